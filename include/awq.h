@@ -63,7 +63,7 @@
 extern "C" {
 #endif
 
-#define AWQ_ABI_VERSION 8
+#define AWQ_ABI_VERSION 9
 
 #if defined(__GNUC__)
 #define AWQ_API __attribute__((visibility("default")))
@@ -450,13 +450,167 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
                                     uint16_t* W_out, void* stream);
 
 /*
+ * ---------------------------------------------------------------------------
+ * The 8-bit paged KV cache: what a decoder layer needs between its q, k and
+ * v products and its output product ("AutoAWQ" code tour, "The Quantization
+ * Flow Up Close": the fused attention block takes the concatenated q, k, v
+ * projection, turns q and k by their positions, keeps a cache of keys and
+ * values and attends over it).
+ *
+ * A cache is n_pages pages of page_size tokens; a page holds, for each key /
+ * value head, its tokens' codes one after another, and one fp32 scale per
+ * AWQ_KV_BLOCK (16) tokens:
+ *
+ *   k_pages, v_pages    uint8 [n_pages][n_kv_heads][page_size][head_dim]
+ *   k_scales, v_scales  fp32  [n_pages][n_kv_heads][page_size / 16]
+ *
+ * pages page_stride bytes and scale_stride floats apart (the rest is dense),
+ * so a layer's pages may be a slice of a larger array. A held value is
+ *   AWQ_KV_INT8: s * (code - 128), codes 1 .. 255
+ *   AWQ_KV_E4M3: s * e4m3(code)
+ * head_dim is 64 or 128; page_size a multiple of 16, up to 65536.
+ *
+ * A batch says which tokens a call is about. Sequence b holds seq_lens[b]
+ * tokens, this call's included; its last n_b = q_indptr[b+1] - q_indptr[b]
+ * tokens are rows q_indptr[b] .. of the call's row arrays, row i at position
+ * seq_lens[b] - n_b + i. Position p is token p % page_size of page
+ * block_table[b][p / page_size]. All three arrays are device memory, read
+ * when the kernels run, so one captured call serves growing sequences. n_b
+ * may be 0; rows whose position is negative (seq_lens[b] < n_b, for instance
+ * a padded entry with seq_lens[b] = 0) have no tokens: the cache and q_out
+ * are not written for them and their attention output is 0. Rows at and
+ * after q_indptr[n_seqs] are neither read nor written.
+ * Sequences may share pages that no sequence writes in the call.
+ *
+ * Values out of range in these arrays (a page id outside 0 .. n_pages - 1, a
+ * length above max_pages * page_size, offsets that descend or pass n_tokens)
+ * never lead outside the buffers: the tokens they concern are skipped, bit 4
+ * of awq_device_error is set, and the outputs of the sequences concerned are
+ * unspecified.
+ *
+ * 16-bit rows (q, k, v, outputs) have their heads x head_dim values dense,
+ * rows `stride` values apart (a multiple of 8), so the columns of a fused
+ * q, k, v product serve as they are; dtype names their type. Positions and
+ * lengths are below 2^31 - 65536; element offsets are 64-bit.
+ */
+#define AWQ_KV_BLOCK 16
+
+#define AWQ_KV_INT8 0   /* awq_kv_cache_t.format */
+#define AWQ_KV_E4M3 1
+
+#define AWQ_KV_FP16 0   /* dtype of the 16-bit rows */
+#define AWQ_KV_BF16 1
+
+typedef struct awq_kv_cache {
+  uint8_t* k_pages;
+  uint8_t* v_pages;
+  float* k_scales;
+  float* v_scales;
+  int64_t n_pages;
+  int64_t page_stride;     /* bytes between pages, a multiple of 16 */
+  int64_t scale_stride;    /* floats between the scales of two pages */
+  int32_t n_kv_heads;
+  int32_t head_dim;
+  int32_t page_size;
+  int32_t format;
+} awq_kv_cache_t;
+
+typedef struct awq_kv_batch {
+  const int32_t* block_table;   /* [n_seqs][max_pages], rows table_stride apart */
+  const int32_t* seq_lens;      /* [n_seqs] */
+  const int32_t* q_indptr;      /* [n_seqs + 1] */
+  int64_t table_stride;
+  int32_t n_seqs;
+  int32_t max_pages;
+  int32_t max_q_len;            /* bound on every n_b; 0: n_tokens is the bound */
+} awq_kv_batch_t;
+
+/* Angles of the rotation: row p of `table` holds the cosines, then the sines
+ * of position p's rot_dim / 2 angles (fp32; rows row_stride floats apart).
+ * The first rot_dim channels of a head turn in pairs (i, i + rot_dim / 2), or
+ * (2i, 2i + 1) when interleaved is 1. rot_dim: a multiple of 16, 16 ..
+ * head_dim. Positions at and after n_positions count as out of range. */
+typedef struct awq_kv_rope {
+  const float* table;
+  int64_t row_stride;
+  int64_t n_positions;
+  int32_t rot_dim;
+  int32_t interleaved;
+} awq_kv_rope_t;
+
+/*
+ * awq_kv_append -- write the batch's keys and values into the cache, k (and
+ * q) turned by their positions on the way.
+ * For each sequence, head and aligned block of 16 positions that gets tokens:
+ *   s  = max(max|x| over the block's new tokens / R, s_old, 2^-60)
+ *   c  = round(x / s)              R = 127 (INT8) or 448 (E4M3)
+ * where x are the (rotated) values in fp32 and s_old is the block's scale if
+ * it holds earlier tokens of the sequence, else 0. If s > s_old their codes
+ * c_old become round(c_old s_old / s). s is held in fp32 (top / R rounded
+ * once); the quotients by it are rounded to nearest even exactly and clamped
+ * to the codes' range. Appending the same rows at
+ * the same positions again leaves the same cache.
+ * k, v [n_tokens][n_kv_heads][head_dim]. q [n_tokens][n_q_heads][head_dim]
+ * and q_out (the same shape; may be q itself) are both given or both NULL;
+ * q_out = q turned, rounded once. rope NULL: nothing is turned. Only the
+ * blocks touched are written. Two sequences of a batch must not write to
+ * the same page.
+ */
+AWQ_API awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
+                                   int32_t dtype, const uint16_t* k, int64_t k_stride, const uint16_t* v,
+                                   int64_t v_stride, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,
+                                   const awq_kv_rope_t* rope, uint16_t* q_out, int64_t q_out_stride, void* stream);
+
+/*
+ * awq_kv_dequant -- the values that the cache holds for the batch's rows:
+ * k_out, v_out [n_tokens][n_kv_heads][head_dim] (dense), each value one
+ * rounding of s * code to dtype. Rows without a token are not written.
+ */
+AWQ_API awq_status_t awq_kv_dequant(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
+                                    int32_t dtype, uint16_t* k_out, uint16_t* v_out, void* stream);
+
+/*
+ * awq_kv_attention -- causal attention of the batch's rows over the cache.
+ * Row i of sequence b at position p, query head h (key / value head
+ * h / (n_q_heads / n_kv_heads)):
+ *   out = sum_j w_j v_j,  w = softmax over the visible j of scale * (q . k_j)
+ * Position j is visible if j <= p and, with window > 0, j > p - window or
+ * j < sinks (the last `window` tokens, p's own among them, and the first
+ * `sinks`). A row that sees nothing gives 0. The batch's own tokens must be
+ * in the cache (awq_kv_append first). The codes enter the products exactly;
+ * q enters as it is (bf16 q through fp16 over a power of two per row, exact
+ * for magnitudes down to 2^-17 of the row's largest); logits, softmax
+ * statistics and sums are fp32; the weights, times the block's value scale,
+ * are rounded to fp16 against a running maximum before they meet the value
+ * codes.
+ * q, out [n_tokens][n_q_heads][head_dim]; n_q_heads a multiple of
+ * n_kv_heads; window, sinks >= 0 (sinks is ignored without a window);
+ * scale finite. out must not overlap q.
+ * workspace: awq_kv_attention_workspace_bytes() bytes of device memory,
+ * 16-byte aligned, contents irrelevant; the size depends on the shapes in
+ * cache, batch and n_q_heads and on the device, not on the lengths. Nothing
+ * in it outlives the call. Calls that may run concurrently need separate
+ * workspaces. The summation order is fixed for given lengths on a given
+ * device: same inputs, same bits.
+ */
+AWQ_API awq_status_t awq_kv_attention_workspace_bytes(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch,
+                                                      int64_t n_tokens, int32_t n_q_heads, size_t* bytes);
+AWQ_API awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
+                                      int32_t dtype, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,
+                                      float scale, int32_t window, int32_t sinks, uint16_t* out, int64_t out_stride,
+                                      void* workspace, size_t workspace_bytes, void* stream);
+
+/*
  * awq_device_error -- read and clear the device-side error word of the
  * current device (synchronizes `stream`). Bit 0: a pipeline wait inside
  * awq_gemm passed its time limit (2 s) and the kernel abandoned its tiles;
  * bit 1: the same inside awq_gemv; bit 2: a pipeline or dependency wait
- * inside awq_gemv_chain. The output is then incomplete. 0 means
- * no error was recorded. No kernel traps: a wait that gives up records the
- * bit, lets its copies in flight land, frees what it holds and returns.
+ * inside awq_gemv_chain; bit 3: a pipeline wait inside awq_kv_attention. The
+ * output is then incomplete. Bit 4: awq_kv_append, awq_kv_dequant or
+ * awq_kv_attention met a page id, length, offset or position out of range
+ * and skipped what it concerns. 0 means no error was recorded.
+ * No kernel traps: a wait that gives up records the bit, lets its copies in
+ * flight land, frees what it holds and returns.
  */
 AWQ_API awq_status_t awq_device_error(uint32_t* error_word, void* stream);
 

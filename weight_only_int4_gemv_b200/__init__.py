@@ -26,7 +26,8 @@ __all__ = [
     "awq_pseudo_quantize_pack", "awq_dequant", "awq_workspace_bytes",
     "awq_gemv", "awq_gemm", "awq_device_error", "awq_linear", "GEMV_MAX_M", "awq_gemv_noalloc",
     "awq_pack_zeros", "awq_unpack_zeros", "validate_product", "GemvChain", "awq_gemv_chain",
-    "CHAIN_MAX_LAYERS",
+    "CHAIN_MAX_LAYERS", "KvCache", "KvBatch", "awq_kv_append", "awq_kv_dequant", "awq_kv_attention",
+    "awq_kv_attention_workspace_bytes", "KV_BLOCK",
 ]
 
 LIB_PATH = os.path.join(os.path.dirname(os.path.abspath(__file__)), "libawq_b200.so")
@@ -44,7 +45,7 @@ class AwqError(RuntimeError):
         self.status = status
 
 
-ABI_VERSION = 8   # awq_abi_version() of a library this binding matches
+ABI_VERSION = 9   # awq_abi_version() of a library this binding matches
 
 
 class QConfig(ctypes.Structure):
@@ -67,6 +68,32 @@ class GemvLayer(ctypes.Structure):
 
 
 CHAIN_MAX_LAYERS = 32
+
+KV_BLOCK = 16                               # tokens of a KV cache that share one scale
+KV_FORMATS = {"int8": 0, "e4m3": 1}
+_KV_DTYPES = {torch.float16: 0, torch.bfloat16: 1}
+
+
+class KvCacheArgs(ctypes.Structure):
+    """awq_kv_cache_t."""
+    _fields_ = [("k_pages", ctypes.c_void_p), ("v_pages", ctypes.c_void_p), ("k_scales", ctypes.c_void_p),
+                ("v_scales", ctypes.c_void_p), ("n_pages", ctypes.c_int64), ("page_stride", ctypes.c_int64),
+                ("scale_stride", ctypes.c_int64), ("n_kv_heads", ctypes.c_int32), ("head_dim", ctypes.c_int32),
+                ("page_size", ctypes.c_int32), ("format", ctypes.c_int32)]
+
+
+class KvBatchArgs(ctypes.Structure):
+    """awq_kv_batch_t."""
+    _fields_ = [("block_table", ctypes.c_void_p), ("seq_lens", ctypes.c_void_p), ("q_indptr", ctypes.c_void_p),
+                ("table_stride", ctypes.c_int64), ("n_seqs", ctypes.c_int32), ("max_pages", ctypes.c_int32),
+                ("max_q_len", ctypes.c_int32)]
+
+
+class KvRopeArgs(ctypes.Structure):
+    """awq_kv_rope_t."""
+    _fields_ = [("table", ctypes.c_void_p), ("row_stride", ctypes.c_int64), ("n_positions", ctypes.c_int64),
+                ("rot_dim", ctypes.c_int32), ("interleaved", ctypes.c_int32)]
+
 
 _lib = None
 _lock = threading.Lock()
@@ -100,6 +127,13 @@ _SIGS = {
                                                       ctypes.POINTER(ctypes.c_size_t)]),
     "awq_gemv_chain": (ctypes.c_int, [ctypes.POINTER(GemvLayer), ctypes.c_int, _I64, _P, ctypes.c_size_t, _P]),
     "awq_debug_set_wait_limit_ns": (ctypes.c_int, [ctypes.c_uint64, _P]),
+    "awq_kv_append": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32, _P, _I64, _P, _I64, _P, _I64, ctypes.c_int32, _P,
+                                     _P, _I64, _P]),
+    "awq_kv_dequant": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32, _P, _P, _P]),
+    "awq_kv_attention_workspace_bytes": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32,
+                                                        ctypes.POINTER(ctypes.c_size_t)]),
+    "awq_kv_attention": (ctypes.c_int, [_P, _P, _I64, ctypes.c_int32, _P, _I64, ctypes.c_int32, ctypes.c_float,
+                                        ctypes.c_int32, ctypes.c_int32, _P, _I64, _P, ctypes.c_size_t, _P]),
 }
 
 
@@ -635,3 +669,246 @@ def awq_debug_set_wait_limit_ns(ns: int, device=None):
     dev = device if device is not None else torch.cuda.current_device()
     with torch.cuda.device(dev):
         _check("awq_debug_set_wait_limit_ns", lib().awq_debug_set_wait_limit_ns(int(ns), _stream(dev)))
+
+
+class KvCache:
+    """The 8-bit paged KV cache of one layer (awq.h): pages of codes and one
+    fp32 scale per head and block of 16 tokens, on one device.
+
+    k_pages, v_pages    uint8 [n_pages, n_kv_heads, page_size, head_dim]
+    k_scales, v_scales  fp32 [n_pages, n_kv_heads, page_size / 16]
+    format              "int8" (codes offset by 128) or "e4m3"
+
+    Pages may lie apart (a slice of an array that holds several layers): only
+    the first dimension may be strided, alike for keys and values. The
+    tensors are the caller's; KvCache.allocate makes a cache of its own."""
+
+    __slots__ = ("k_pages", "v_pages", "k_scales", "v_scales", "format", "n_kv_heads", "head_dim", "page_size",
+                 "device", "_args", "_ref")
+
+    def __init__(self, k_pages, v_pages, k_scales, v_scales, format: str = "int8"):
+        if format not in KV_FORMATS:
+            raise ValueError(f"format must be one of {sorted(KV_FORMATS)}, got {format!r}")
+        for name, t, dtype, ndim in (("k_pages", k_pages, torch.uint8, 4), ("v_pages", v_pages, torch.uint8, 4),
+                                     ("k_scales", k_scales, torch.float32, 3),
+                                     ("v_scales", v_scales, torch.float32, 3)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != dtype:
+                raise TypeError(f"{name} must be {dtype}, got {t.dtype}")
+            if t.dim() != ndim:
+                raise ValueError(f"{name} must be a {ndim}-d tensor")
+            if not t[:1].is_contiguous() or t.device != k_pages.device:
+                raise ValueError(f"{name} must be dense within a page and on {k_pages.device}")
+        n, heads, page, dim = k_pages.shape
+        if v_pages.shape != k_pages.shape:
+            raise ValueError("k_pages and v_pages must have the same shape")
+        if tuple(k_scales.shape) != (n, heads, page // KV_BLOCK) or v_scales.shape != k_scales.shape:
+            raise ValueError("k_scales and v_scales must be [n_pages, n_kv_heads, page_size / 16]")
+        # (a single page's stride means nothing: the dense one is as good)
+        strides = (k_pages.stride(0), k_scales.stride(0)) if n > 1 else (heads * page * dim, k_scales[:1].numel())
+        if n > 1 and (v_pages.stride(0), v_scales.stride(0)) != strides:
+            raise ValueError("keys and values must have the same stride between pages")
+        self.k_pages, self.v_pages, self.k_scales, self.v_scales = k_pages, v_pages, k_scales, v_scales
+        self.format, self.n_kv_heads, self.head_dim, self.page_size = format, heads, dim, page
+        self.device = k_pages.device
+        self._args = KvCacheArgs(k_pages.data_ptr(), v_pages.data_ptr(), k_scales.data_ptr(), v_scales.data_ptr(), n,
+                                 strides[0], strides[1], heads, dim, page, KV_FORMATS[format])
+        self._ref = ctypes.addressof(self._args)
+
+    @classmethod
+    def allocate(cls, n_pages: int, n_kv_heads: int, page_size: int, head_dim: int, format: str = "int8",
+                 device=None) -> "KvCache":
+        """A cache of n_pages pages (contents unspecified: nothing is read before it is written)."""
+        device = torch.device(device) if device is not None else torch.device("cuda", torch.cuda.current_device())
+        if page_size <= 0 or page_size % KV_BLOCK:
+            raise ValueError("page_size must be a positive multiple of 16")
+        pages = [torch.zeros((n_pages, n_kv_heads, page_size, head_dim), dtype=torch.uint8, device=device)
+                 for _ in range(2)]
+        scales = [torch.zeros((n_pages, n_kv_heads, page_size // KV_BLOCK), device=device) for _ in range(2)]
+        return cls(*pages, *scales, format)
+
+
+class KvBatch:
+    """Which tokens a KV-cache call is about (awq.h): sequence b holds
+    seq_lens[b] tokens, this call's included; its last q_indptr[b+1] -
+    q_indptr[b] tokens are rows q_indptr[b] .. of the call's row tensors.
+
+    block_table  int32 [n_seqs, max_pages] page ids
+    seq_lens     int32 [n_seqs]
+    q_indptr     int32 [n_seqs + 1], from 0
+    max_q_len    the most rows of one sequence (None: no bound known)
+
+    The tensors are read when the kernels run: a decode loop (or a captured
+    graph) updates them in place and keeps the object for every layer."""
+
+    __slots__ = ("block_table", "seq_lens", "q_indptr", "max_q_len", "device", "_args", "_ref")
+
+    def __init__(self, block_table, seq_lens, q_indptr, max_q_len: int | None = None):
+        for name, t, ndim in (("block_table", block_table, 2), ("seq_lens", seq_lens, 1), ("q_indptr", q_indptr, 1)):
+            if not isinstance(t, torch.Tensor):
+                raise TypeError(f"{name} must be a torch.Tensor")
+            if t.dtype != torch.int32:
+                raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
+            if t.dim() != ndim or (t.numel() > 1 and t.stride(-1) != 1):
+                raise ValueError(f"{name} must be a {ndim}-d tensor with dense rows")
+            if t.device != block_table.device:
+                raise ValueError(f"{name} is on {t.device}, block_table on {block_table.device}")
+        n, pages = block_table.shape
+        if seq_lens.shape[0] != n or q_indptr.shape[0] != n + 1:
+            raise ValueError("seq_lens must be [n_seqs] and q_indptr [n_seqs + 1] for block_table [n_seqs, max_pages]")
+        if n > 1 and block_table.stride(0) < pages:
+            raise ValueError("the rows of block_table must not overlap")
+        if max_q_len is not None and not 1 <= max_q_len < 2 ** 31:
+            raise ValueError("max_q_len must be positive, or None")
+        self.block_table, self.seq_lens, self.q_indptr, self.max_q_len = block_table, seq_lens, q_indptr, max_q_len
+        self.device = block_table.device
+        self._args = KvBatchArgs(block_table.data_ptr(), seq_lens.data_ptr(), q_indptr.data_ptr(),
+                                 block_table.stride(0) if n > 1 else pages, n, pages, max_q_len or 0)
+        self._ref = ctypes.addressof(self._args)
+
+
+def _kv_rows(t, name: str, cache: KvCache, heads: int | None, rows: int | None, dtype):
+    """One 16-bit row tensor [tokens, heads, head_dim] of a KV-cache call:
+    heads and channels dense, rows any stride. Returns that stride."""
+    if not isinstance(t, torch.Tensor):
+        raise TypeError(f"{name} must be a torch.Tensor")
+    if t.dtype not in _KV_DTYPES or (dtype is not None and t.dtype != dtype):
+        raise TypeError(f"{name} must be {dtype or 'torch.float16 or torch.bfloat16'}, got {t.dtype}")
+    if not t.is_cuda:
+        raise ValueError(f"{name} must be a CUDA tensor (no CPU path exists)")
+    shape = t.shape
+    if len(shape) != 3 or shape[2] != cache.head_dim or (heads is not None and shape[1] != heads) or \
+            (rows is not None and shape[0] != rows):
+        want = f"[{'tokens' if rows is None else rows}, {'heads' if heads is None else heads}, {cache.head_dim}]"
+        raise ValueError(f"{name} must be {want}, got {list(shape)}")
+    stride, sh, sd = t.stride()
+    if sd != 1 or (sh != cache.head_dim and shape[1] > 1):
+        raise ValueError(f"the heads of a row of {name} must be dense")
+    if t.device != cache.device:
+        raise ValueError(f"{name} is on {t.device}, the cache on {cache.device}")
+    return stride if shape[0] > 1 else shape[1] * cache.head_dim
+
+
+def _kv_call(entry: str, cache: KvCache, batch: KvBatch, *args):
+    if batch.device != cache.device:
+        raise ValueError(f"the batch is on {batch.device}, the cache on {cache.device}")
+    fn = getattr(lib(), entry)
+    dev = cache.device
+    if dev.index == torch.cuda.current_device():
+        st = fn(cache._ref, batch._ref, *args, torch.cuda.current_stream().cuda_stream)
+    else:
+        with torch.cuda.device(dev):
+            st = fn(cache._ref, batch._ref, *args, torch.cuda.current_stream(dev).cuda_stream)
+    if st != AWQ_OK:
+        _check(entry, st)
+
+
+def awq_kv_append(k, v, cache: KvCache, batch: KvBatch, q=None, rope=None, interleaved: bool = False, q_out=None):
+    """Write the batch's keys and values [tokens, n_kv_heads, head_dim] (fp16
+    or bf16; slices of a fused product's rows will do) into the cache, k and q
+    turned by their positions on the way. Returns the turned q (q_out, or a
+    new tensor; q_out may be q), None without q.
+
+    rope: fp32 [positions, rot_dim], each row the cosines, then the sines of
+    its position's rot_dim / 2 angles; None: nothing is turned. Channel pairs
+    are (i, i + rot_dim / 2), or (2i, 2i + 1) with interleaved."""
+    ks = _kv_rows(k, "k", cache, cache.n_kv_heads, None, None)
+    rows, dtype = k.shape[0], k.dtype
+    vs = _kv_rows(v, "v", cache, cache.n_kv_heads, rows, dtype)
+    qp = op = None
+    qs = os_ = heads = 0
+    if q is not None:
+        qs = _kv_rows(q, "q", cache, None, rows, dtype)
+        heads = q.shape[1]
+        if q_out is None:
+            q_out = torch.empty((rows, heads, cache.head_dim), dtype=dtype, device=q.device)
+        os_ = _kv_rows(q_out, "q_out", cache, heads, rows, dtype)
+        qp, op = q.data_ptr(), q_out.data_ptr()
+    elif q_out is not None:
+        raise ValueError("q_out without q")
+    args = rp = None
+    if rope is not None:
+        if not isinstance(rope, torch.Tensor):
+            raise TypeError("rope must be a torch.Tensor")
+        if rope.dtype != torch.float32:
+            raise TypeError(f"rope must be torch.float32, got {rope.dtype}")
+        if rope.dim() != 2 or rope.stride(1) != 1:
+            raise ValueError("rope must be a 2-d tensor with dense rows")
+        if rope.device != cache.device:
+            raise ValueError(f"rope is on {rope.device}, the cache on {cache.device}")
+        n, rot = rope.shape
+        args = KvRopeArgs(rope.data_ptr(), rope.stride(0) if n > 1 else rot, n, rot, 1 if interleaved else 0)
+        rp = ctypes.addressof(args)
+    _kv_call("awq_kv_append", cache, batch, rows, _KV_DTYPES[dtype], k.data_ptr(), ks, v.data_ptr(), vs, qp, qs, heads,
+             rp, op, os_)
+    return q_out
+
+
+def awq_kv_dequant(cache: KvCache, batch: KvBatch, n_tokens: int, dtype: torch.dtype = torch.float16, k_out=None,
+                   v_out=None):
+    """The values that the cache holds for the batch's rows: (keys, values),
+    each [n_tokens, n_kv_heads, head_dim] in dtype (rows without a token are
+    not written)."""
+    if dtype not in _KV_DTYPES:
+        raise TypeError(f"dtype must be torch.float16 or torch.bfloat16, got {dtype}")
+    shape = (n_tokens, cache.n_kv_heads, cache.head_dim)
+    outs = []
+    for name, t in (("k_out", k_out), ("v_out", v_out)):
+        if t is None:
+            t = torch.empty(shape, dtype=dtype, device=cache.device)
+        elif _kv_rows(t, name, cache, cache.n_kv_heads, n_tokens, dtype) != shape[1] * shape[2]:
+            raise ValueError(f"{name} must be contiguous")
+        outs.append(t)
+    _kv_call("awq_kv_dequant", cache, batch, n_tokens, _KV_DTYPES[dtype], outs[0].data_ptr(), outs[1].data_ptr())
+    return outs[0], outs[1]
+
+
+def awq_kv_attention_workspace_bytes(cache: KvCache, batch: KvBatch, n_tokens: int, n_q_heads: int) -> int:
+    """Workspace bytes of awq_kv_attention for these shapes on the cache's device."""
+    n = ctypes.c_size_t(0)
+    with torch.cuda.device(cache.device):
+        _check("awq_kv_attention_workspace_bytes", lib().awq_kv_attention_workspace_bytes(
+            cache._ref, batch._ref, n_tokens, n_q_heads, ctypes.byref(n)))
+    return int(n.value)
+
+
+def awq_kv_attention(q, cache: KvCache, batch: KvBatch, scale: float | None = None, window: int = 0, sinks: int = 0,
+                     out=None, workspace=None):
+    """Causal attention of the batch's rows q [tokens, n_q_heads, head_dim]
+    over the cache (append the batch's own tokens first); out has q's shape.
+
+    scale: of the logits (None: head_dim ** -0.5). window > 0: a row sees the
+    last `window` positions, its own among them, and the first `sinks`. Rows
+    that see nothing give 0.
+    workspace: a uint8 tensor of awq_kv_attention_workspace_bytes(), contents
+    irrelevant (None: allocated for the call); calls that may overlap on the
+    device need separate ones."""
+    qs = _kv_rows(q, "q", cache, None, None, None)
+    rows, heads, dim = q.shape
+    if not 0 <= window < 2 ** 31 or not 0 <= sinks < 2 ** 31:
+        raise ValueError("window and sinks must be non-negative 32-bit integers")
+    if out is None:
+        out = torch.empty((rows, heads, dim), dtype=q.dtype, device=q.device)
+        os_ = heads * dim
+    else:
+        os_ = _kv_rows(out, "out", cache, heads, rows, q.dtype)
+    if workspace is None:
+        # the size goes by shapes and the device alone: asked for once per kind of call
+        key = (cache.device, cache._args.head_dim, cache._args.format, cache.n_kv_heads, cache.page_size,
+               batch._args.n_seqs, batch._args.max_pages, batch._args.max_q_len, rows, heads)
+        n = _kv_workspace.get(key)
+        if n is None:
+            if len(_kv_workspace) > 4096:
+                _kv_workspace.clear()
+            n = _kv_workspace[key] = awq_kv_attention_workspace_bytes(cache, batch, rows, heads)
+        workspace = torch.empty(n, dtype=torch.uint8, device=q.device)
+    elif not isinstance(workspace, torch.Tensor) or not workspace.is_contiguous() or workspace.device != q.device:
+        raise ValueError(f"workspace must be a contiguous tensor on {q.device}")
+    _kv_call("awq_kv_attention", cache, batch, rows, _KV_DTYPES[q.dtype], q.data_ptr(), qs, heads,
+             dim ** -0.5 if scale is None else float(scale), window, sinks, out.data_ptr(), os_, workspace.data_ptr(),
+             workspace.numel() * workspace.element_size())
+    return out
+
+
+_kv_workspace: dict = {}

@@ -76,6 +76,10 @@ namespace gemm128s {   // 128-channel tiles and 128-row x tiles, for M <= 128
 
 awq_status_t gemv_take_error(uint32_t* word, cudaStream_t s);
 awq_status_t chain_take_error(uint32_t* word, cudaStream_t s);
+namespace kv {
+awq_status_t append_take_error(uint32_t* word, cudaStream_t s);
+awq_status_t attention_take_error(uint32_t* word, cudaStream_t s);
+}  // namespace kv
 
 awq_status_t gemm_workspace_bytes(int64_t, int64_t, int64_t, bool, size_t* bytes) {
   *bytes = 0;
@@ -147,6 +151,9 @@ extern "C" awq_status_t awq_device_error(uint32_t* error_word, void* stream) {
   if (st != AWQ_OK) return st;
   uint32_t chain_word = 0;
   if ((st = chain_take_error(&chain_word, s)) != AWQ_OK) return st;
-  *error_word = gemm_word | gemv_word | chain_word;
+  uint32_t append_word = 0, attention_word = 0;
+  if ((st = kv::append_take_error(&append_word, s)) != AWQ_OK) return st;
+  if ((st = kv::attention_take_error(&attention_word, s)) != AWQ_OK) return st;
+  *error_word = gemm_word | gemv_word | chain_word | append_word | attention_word;
   return AWQ_OK;
 }

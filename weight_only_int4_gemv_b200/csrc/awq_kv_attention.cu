@@ -1,0 +1,838 @@
+// awq_kv_attention: attention over the 8-bit paged KV cache.
+//
+// Mathematics. One key / value head serves group = n_q_heads / n_kv_heads
+// query heads, so the rows of a sequence and head are the (token, head of the
+// group) pairs, R of them to a tile. For a tile of 16 keys (one scale block)
+//   S = K_codes q^T            exact products, fp32 sums (tensor cores)
+//   t_j = scale log2(e) s_k S_j + log2(s_v)
+//   p_j = 2^(t_j - m),  O += V_codes^T p,  l += p_j / s_v
+// with a running maximum m of t, and y = O / l at the end: the value scale
+// rides on the weight (sum 2^(t'_j) s_v c_j / sum 2^(t'_j), t' = t - log2
+// s_v), so the codes enter the second product as they are, and p <= 2^8 fits
+// fp16 whatever the scales. m is only raised when a logit passes it by more
+// than 8 (then O and l are rescaled); below that p stays within fp16.
+//
+// What bounds it: for the few rows of decoding, reading the cache. Both
+// products have the codes as the 16-row operand of mma.sync.m16n8k16 (16 keys
+// or 16 channels by 16) and the rows as its 8 columns, fed from registers:
+// a code is used once per row tile, so writing its 16-bit form to shared
+// memory for a tcgen05 operand would cost several times the bytes read from
+// HBM, as in the GEMV. The transposition of S into the second product's
+// operand is one movmatrix per 8 keys; the channel order of both operands is
+// chosen so that a lane's codes are 16 contiguous bytes, and the TMA's
+// swizzle makes those reads free of bank conflicts.
+//
+// Split. All (sequence, row tile, head) items are laid end to end as units of
+// 16 keys and cut into equal runs, one per resident CTA, whatever the
+// lengths; the cut is computed by every CTA from the lengths in device memory.
+// An item that lies within one CTA's run is written out directly. Of an item
+// that spans several, each writes (m, l, O) to the workspace, and a second
+// kernel joins them in order; it needs no counters, so the workspace carries
+// no state.
+//
+// In a CTA one producer warp looks up pages and issues the TMA copies (a box
+// of 16 tokens x head_dim per copy) and four consumer warps take one 16-key
+// tile of each stage, each with its own m, l and O, joined at the item's end.
+
+#include <cuda.h>
+#include <cudaTypedefs.h>
+
+#include <atomic>
+#include <type_traits>
+
+#include "awq_kv.cuh"
+#include "awq_tma_host.h"
+
+namespace awq {
+namespace kv {
+namespace {
+
+__device__ uint32_t g_kv_attention_error = 0;
+
+constexpr int W = 4;                       // consumer warps
+constexpr int kThreads = (W + 1) * 32;
+constexpr int kStages = 3;
+constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
+
+struct AttentionParams {
+  Batch batch;
+  const uint16_t* q;
+  uint16_t* out;
+  int64_t q_stride, out_stride;
+  const float* k_scales;
+  const float* v_scales;
+  int64_t scale_stride;
+  float scale_log2;
+  int32_t window, sinks;
+  int32_t group, n_kv_heads;
+  float* part;                             // [2 grid][R][D + 2] fp32
+  struct Join* joins;                      // [grid]
+};
+
+// A split item, described by the CTA in whose run it starts.
+struct Join {
+  int32_t last;      // CTA in whose run it ends; -1: no such item
+  int32_t slot;      // its first part
+  int32_t t0, row0, rows, head;
+  int32_t pad[2];
+};
+
+// The keys that a sequence's rows may see: sink tiles, then the tiles from w0.
+struct Span {
+  int tiles, sink_tiles, w0, row_tiles;
+};
+
+template <int R>
+__device__ __forceinline__ Span span_of(const AttentionParams& p, const Seq& s) {
+  Span a;
+  if (s.n == 0) {
+    a.tiles = a.sink_tiles = a.w0 = a.row_tiles = 0;
+    return a;
+  }
+  const int low = p.window ? max(0, s.past - p.window + 1) : 0;
+  a.w0 = min(low, s.len) / kBlock;
+  a.sink_tiles = p.window ? min((min(p.sinks, low) + kBlock - 1) / kBlock, a.w0) : 0;
+  a.tiles = max(a.sink_tiles + (s.len + kBlock - 1) / kBlock - a.w0, 1);   // one for a row that sees nothing
+  a.row_tiles = int((int64_t(s.n) * p.group + R - 1) / R);
+  return a;
+}
+
+template <int D, int R>
+struct Shared {
+  static constexpr int kTile = kBlock * D;              // bytes of 16 keys or values
+  static constexpr int kStageBytes = 2 * W * kTile;
+  static constexpr int kMergeRow = D + 4;
+  struct Meta {
+    int tile[W];            // position of the tile's first key, -1: nothing there
+    float ks[W], vs[W];
+    int cnt, first, last, t0, row0, rows, past, head, dest;
+  };
+  uint8_t ring[kStages][kStageBytes];
+  float merge[W][R][kMergeRow];
+  float stat[W][R][2];
+  Meta meta[kStages];
+  uint64_t full[kStages], empty[kStages], merged, taken;
+  int64_t scratch[40];
+  int abort;
+};
+
+__device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
+  asm volatile(
+      "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0,%1,%2,%3}, {%4,%5,%6,%7}, {%8,%9}, {%0,%1,%2,%3};"
+      : "+f"(c[0]), "+f"(c[1]), "+f"(c[2]), "+f"(c[3])
+      : "r"(a[0]), "r"(a[1]), "r"(a[2]), "r"(a[3]), "r"(b0), "r"(b1));
+}
+
+__device__ __forceinline__ uint32_t transpose8x8(uint32_t v) {
+  uint32_t r;
+  asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(v));
+  return r;
+}
+
+__device__ __forceinline__ float exp2_fast(float x) {
+  float r;
+  asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+  return r;
+}
+
+// Two codes (bytes LO, LO + 1 of w) as an fp16 pair, exactly. int8: a byte u
+// under 0x64 is the fp16 number 1024 + u = 1152 + code.
+template <int FMT, int LO>
+__device__ __forceinline__ uint32_t code_pair(uint32_t w) {
+  if constexpr (FMT == AWQ_KV_INT8) {
+    return hsub2_u32(__byte_perm(w, 0x64646464u, LO ? 0x4342 : 0x4140), 0x64806480u);
+  } else {
+    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(LO ? w >> 16 : w & 0xffffu), __NV_E4M3);
+    return uint32_t(r.x) | (uint32_t(r.y) << 16);
+  }
+}
+
+// Row tile `row0` of q as the products' column operand: lane (n, t) holds
+// channels [D/4 t, D/4 (t + 1)) of row n. bf16 rows are brought to fp16 over
+// a power of two of their largest magnitude, returned in `factor` (of row n).
+template <typename T, int D>
+__device__ __forceinline__ void load_q(const AttentionParams& p, int t0, int row, bool there, int head, int t,
+                                       uint32_t (&f)[D / 8], float& factor) {
+  uint4 raw[D / 32];
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
+  if (there) {
+    const uint16_t* src =
+        p.q + int64_t(t0 + row / p.group) * p.q_stride + int64_t(head * p.group + row % p.group) * D + t * (D / 4);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) raw[i] = reinterpret_cast<const uint4*>(src)[i];
+  }
+  factor = 1.0f;
+  if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+    float x[D / 32][8], top = 0.0f;
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+      unpack8<T>(raw[i], x[i]);
+#pragma unroll
+      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i][j]));
+    }
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+    top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+    // 2^e <= top: its exponent field alone, kept where the reciprocal is a normal number too
+    const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+    factor = __uint_as_float(e << 23);
+    const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+    for (int i = 0; i < D / 32; ++i) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) x[i][j] *= inv;
+      raw[i] = pack8<__half>(x[i]);
+    }
+  }
+#pragma unroll
+  for (int i = 0; i < D / 32; ++i) {
+    f[4 * i] = raw[i].x;
+    f[4 * i + 1] = raw[i].y;
+    f[4 * i + 2] = raw[i].z;
+    f[4 * i + 3] = raw[i].w;
+  }
+}
+
+template <typename T, int D, int FMT, int NT>
+__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                        const __grid_constant__ AttentionParams p) {
+  constexpr int R = 8 * NT;
+  using Sh = Shared<D, R>;
+  extern __shared__ uint8_t smem_raw[];
+  Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &sh.abort;
+  uint32_t* err = &g_kv_attention_error;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kStages; ++i) {
+      mbar_init(&sh.full[i], 33);   // the producer's arrival with the byte count, its lanes' scale copies
+      mbar_init(&sh.empty[i], W);
+    }
+    mbar_init(&sh.merged, W);
+    mbar_init(&sh.taken, W);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  pdl_launch();
+  pdl_wait();
+
+  // this CTA's run of units
+  int64_t per = 0, total = 0, rest = 0;
+  const int b_first = locate(
+      p.batch.n_seqs, sh.scratch,
+      [&](int b) {
+        const Span a = span_of<R>(p, load_seq(p.batch, b, err));
+        return int64_t(a.tiles) * a.row_tiles * p.n_kv_heads;
+      },
+      [&](int64_t sum) {
+        per = (sum + gridDim.x - 1) / gridDim.x;
+        per = (per + W - 1) / W * W;
+        return per * blockIdx.x;
+      },
+      &rest, &total);
+  const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
+
+  if (warp == W) {
+    // ------------------------------------------------------------ producer
+    Join join;
+    join.last = -1;
+    int s = 0;
+    uint32_t ph = 0, used = 0;       // used: stages filled at least once
+    bool ok = true;
+    if (b_first >= 0) {
+      int b = b_first;
+      Seq seq = load_seq(p.batch, b, err);
+      Span a = span_of<R>(p, seq);
+      int item = int(rest / a.tiles), tile = int(rest % a.tiles);
+      int64_t u = u0;
+      // one stage: up to W tiles of one item; lane i < W holds tile i's key copy, lane W + i its value copy
+      struct Stage {
+        int cnt, first, last, t0, row0, rows, past, head, dest, pos, id;
+      };
+      auto next = [&](Stage& st) {
+        while (item >= a.row_tiles * p.n_kv_heads) {   // on to the next sequence with rows
+          seq = load_seq(p.batch, ++b, err);
+          a = span_of<R>(p, seq);
+          item = 0;
+        }
+        const int left = int(min(int64_t(a.tiles - tile), u1 - u));
+        st.cnt = min(W, left);
+        const int64_t begin = u - tile, end = begin + a.tiles;
+        st.first = u == u0 || tile == 0;
+        st.last = st.cnt == left;
+        st.head = item % p.n_kv_heads;
+        st.row0 = item / p.n_kv_heads * R;
+        st.rows = min(R, seq.n * p.group - st.row0);
+        st.t0 = seq.t0;
+        st.past = seq.past;
+        const bool whole = begin >= u0 && end <= u1;
+        st.dest = whole ? -1 : int(2 * blockIdx.x) + (begin > u0);
+        if (begin >= u0 && end > u1) {
+          join.last = int((end - 1) / per);
+          join.slot = st.dest;
+          join.t0 = st.t0;
+          join.row0 = st.row0;
+          join.rows = st.rows;
+          join.head = st.head;
+        }
+        const int i = lane % W, v = tile + i;
+        st.pos = -1;
+        st.id = -1;
+        if (lane < 2 * W && i < st.cnt) {
+          const int pos = (v < a.sink_tiles ? v : v - a.sink_tiles + a.w0) * kBlock;
+          if (pos < seq.len) {
+            st.pos = pos;
+            st.id = p.batch.table[int64_t(b) * p.batch.table_stride + pos / p.batch.page_size];
+          }
+        }
+        u += st.cnt;
+        tile += st.cnt;
+        if (tile == a.tiles) {
+          tile = 0;
+          ++item;
+        }
+      };
+      Stage cur, after;
+      bool more = u < u1;
+      if (more) next(cur);
+      while (more) {
+        more = u < u1;
+        if (more) next(after);         // its page ids load while the current stage is issued
+        if (!wait_sleep(&sh.empty[s], ph ^ 1, abort, err, kErrWait)) {
+          ok = false;
+          break;
+        }
+        int page = -1;
+        if (cur.pos >= 0) page = checked_page(p.batch, cur.id, err);
+        auto& m = sh.meta[s];
+        const int i = lane % W;
+        const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
+        if (lane < W) m.tile[i] = page >= 0 ? cur.pos : -1;
+        if (lane == 0) {
+          m.cnt = cur.cnt;
+          m.first = cur.first;
+          m.last = cur.last;
+          m.t0 = cur.t0;
+          m.row0 = cur.row0;
+          m.rows = cur.rows;
+          m.past = cur.past;
+          m.head = cur.head;
+          m.dest = cur.dest;
+        }
+        __syncwarp();   // the lanes' entries, before the arrival that publishes them
+        if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(__popc(here)) * Sh::kTile);
+        __syncwarp();
+        if (page >= 0) {
+          const bool val = lane >= W;
+          const int off = cur.pos % p.batch.page_size;
+          tma_load_4d(&sh.ring[s][(val ? W * Sh::kTile : 0) + i * Sh::kTile], val ? &map_v : &map_k, 0, off, cur.head,
+                      page, &sh.full[s]);
+          const float* sc = (val ? p.v_scales : p.k_scales) + int64_t(page) * p.scale_stride +
+                            cur.head * (p.batch.page_size / kBlock) + off / kBlock;
+          asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(val ? &m.vs[i] : &m.ks[i])), "l"(sc)
+                       : "memory");
+        }
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s])) : "memory");
+        used |= 1u << s;
+        if (++s == kStages) {
+          s = 0;
+          ph ^= 1;
+        }
+        cur = after;
+      }
+    }
+    if (lane == 0) p.joins[blockIdx.x] = join;
+    if (!ok) {
+      // every copy issued lands before the CTA's shared memory goes
+      for (int i = 0; i < kStages; ++i)
+        if (used & (1u << i)) wait_sleep_teardown(&sh.full[i], i < s ? ph : ph ^ 1);
+    }
+    return;
+  }
+
+  // -------------------------------------------------------------- consumers
+  const int g = lane >> 2, t = lane & 3;
+  uint32_t qf[NT][D / 8];
+  float factor[NT][2];               // of columns 2t, 2t + 1: logit scale in log2 units
+  int at[NT][2];                     // positions of those rows
+  float m[NT][2], l[NT][2];
+  float acc[NT][D / 16][4];
+  int p_low = 0, p_high = 0;
+  int s = 0;
+  uint32_t ph = 0, merges = 0;
+  for (int64_t u = u0; u < u1;) {
+    if (!wait_sleep(&sh.full[s], ph, abort, err, kErrWait)) return;
+    const auto& me = sh.meta[s];
+    const int first = me.first, last = me.last, t0 = me.t0, row0 = me.row0, rows = me.rows, past = me.past,
+              head = me.head, dest = me.dest, cnt = me.cnt, tile = me.tile[warp];
+    if (first) {
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float mine;
+        load_q<T, D>(p, t0, row0 + nt * 8 + g, nt * 8 + g < rows, head, t, qf[nt], mine);
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          factor[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
+          at[nt][e] = past + (row0 + nt * 8 + 2 * t + e) / p.group;
+          m[nt][e] = -INFINITY;
+          l[nt][e] = 0.0f;
+        }
+#pragma unroll
+        for (int j = 0; j < D / 16; ++j)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) acc[nt][j][e] = 0.0f;
+      }
+      p_low = past + row0 / p.group;
+      p_high = past + (row0 + rows - 1) / p.group;
+    }
+    if (tile >= 0) {
+      const uint8_t* kt = &sh.ring[s][warp * Sh::kTile];
+      const uint8_t* vt = &sh.ring[s][(W + warp) * Sh::kTile];
+      const float ks = me.ks[warp], vs = me.vs[warp];
+      // S = K q^T
+      float sc[NT][4];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+#pragma unroll
+      for (int i = 0; i < D / 64; ++i) {
+        uint4 lo, hi;
+        if constexpr (D == 128) {
+          const int c = ((2 * t + i) ^ g) << 4;
+          lo = *reinterpret_cast<const uint4*>(kt + g * 128 + c);
+          hi = *reinterpret_cast<const uint4*>(kt + (g + 8) * 128 + c);
+        } else {
+          const int c = (t ^ (g >> 1)) << 4;
+          lo = *reinterpret_cast<const uint4*>(kt + g * 64 + c);
+          hi = *reinterpret_cast<const uint4*>(kt + (g + 8) * 64 + c);
+        }
+        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+#pragma unroll
+        for (int w = 0; w < 4; ++w) {
+          const uint32_t a[4] = {code_pair<FMT, 0>(wl[w]), code_pair<FMT, 0>(wh[w]), code_pair<FMT, 2>(wl[w]),
+                                 code_pair<FMT, 2>(wh[w])};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[nt][8 * i + 2 * w], qf[nt][8 * i + 2 * w + 1]);
+        }
+      }
+      // weights
+      const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
+      const bool all = tile + kBlock - 1 <= p_low &&
+                       (p.window == 0 || tile > p_high - p.window || tile + kBlock <= p.sinks);
+      bool raise = false;
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          float v = fmaf(sc[nt][e], factor[nt][e & 1] * ks, lv);
+          if (!all) {
+            const int j = tile + g + (e & 2) * 4, q = at[nt][e & 1];
+            if (!(j <= q && (p.window == 0 || j > q - p.window || j < p.sinks))) v = -INFINITY;
+          }
+          sc[nt][e] = v;
+          raise |= v > m[nt][e & 1] + kSlack;
+        }
+      if (__any_sync(0xffffffffu, raise)) {
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) {
+            float v = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
+            v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
+            v = fmaxf(v, m[nt][e]);
+            const float f = v == -INFINITY ? 1.0f : exp2_fast(m[nt][e] - v);
+            m[nt][e] = v;
+            l[nt][e] *= f;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j) {
+              acc[nt][j][e] *= f;
+              acc[nt][j][e + 2] *= f;
+            }
+          }
+      }
+      uint32_t b0[NT], b1[NT];
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt) {
+        float w[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) {
+          const float mm = m[nt][e & 1];
+          w[e] = exp2_fast(sc[nt][e] - (mm == -INFINITY ? 0.0f : mm));
+          l[nt][e & 1] = fmaf(w[e], iv, l[nt][e & 1]);
+        }
+        b0[nt] = transpose8x8(Half16<__half>::pack(w[0], w[1]));
+        b1[nt] = transpose8x8(Half16<__half>::pack(w[2], w[3]));
+      }
+      // O += V^T p: lane (g, t) holds channels [D/8 g, D/8 (g + 1)) of keys 2t, 2t+1, 2t+8, 2t+9
+      uint32_t vw[4][D / 32];
+#pragma unroll
+      for (int i = 0; i < 4; ++i) {
+        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+        if constexpr (D == 128) {
+          const uint4 x = *reinterpret_cast<const uint4*>(vt + r * 128 + ((g ^ (r & 7)) << 4));
+          vw[i][0] = x.x;
+          vw[i][1] = x.y;
+          vw[i][2] = x.z;
+          vw[i][3] = x.w;
+        } else {
+          const uint2 x = *reinterpret_cast<const uint2*>(vt + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+          vw[i][0] = x.x;
+          vw[i][1] = x.y;
+        }
+        // e4m3 bytes behind the sequence's end may be NaN, which a weight of 0 does not silence
+        if (FMT == AWQ_KV_E4M3 && !all && tile + r > p_high) {
+#pragma unroll
+          for (int w = 0; w < D / 32; ++w) vw[i][w] = 0;
+        }
+      }
+#pragma unroll
+      for (int w = 0; w < D / 32; ++w) {
+        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
+        const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
+        const uint32_t a0[4] = {code_pair<FMT, 0>(x0), code_pair<FMT, 2>(x0), code_pair<FMT, 0>(x1),
+                                code_pair<FMT, 2>(x1)};
+        const uint32_t a1[4] = {code_pair<FMT, 0>(y0), code_pair<FMT, 2>(y0), code_pair<FMT, 0>(y1),
+                                code_pair<FMT, 2>(y1)};
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) {
+          mma_16816(acc[nt][2 * w], a0, b0[nt], b1[nt]);
+          mma_16816(acc[nt][2 * w + 1], a1, b0[nt], b1[nt]);
+        }
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.empty[s]);
+    u += cnt;
+    if (++s == kStages) {
+      s = 0;
+      ph ^= 1;
+    }
+    if (!last) continue;
+
+    // join the warps' parts of the item
+    if (merges && !wait_sleep(&sh.taken, (merges - 1) & 1, abort, err, kErrWait)) return;
+#pragma unroll
+    for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+      for (int e = 0; e < 2; ++e) {
+        const int r = nt * 8 + 2 * t + e;
+        float sum = l[nt][e];
+        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+        if (g == 0) {
+          sh.stat[warp][r][0] = m[nt][e];
+          sh.stat[warp][r][1] = sum;
+        }
+        if (r < rows) {
+#pragma unroll
+          for (int j = 0; j < D / 16; ++j)
+            *reinterpret_cast<float2*>(&sh.merge[warp][r][D / 8 * g + 2 * j]) =
+                make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
+        }
+      }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.merged);
+    if (!wait_sleep(&sh.merged, merges & 1, abort, err, kErrWait)) return;
+    for (int i = threadIdx.x; i < rows * (D / 4); i += W * 32) {
+      const int r = i / (D / 4), d = i % (D / 4) * 4;
+      float top = -INFINITY;
+#pragma unroll
+      for (int w = 0; w < W; ++w) top = fmaxf(top, sh.stat[w][r][0]);
+      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+      float sum = 0.0f;
+#pragma unroll
+      for (int w = 0; w < W; ++w) {
+        const float f = top == -INFINITY ? 0.0f : exp2_fast(sh.stat[w][r][0] - top);
+        const float4 x = *reinterpret_cast<const float4*>(&sh.merge[w][r][d]);
+        sum = fmaf(f, sh.stat[w][r][1], sum);
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
+      }
+      if (dest < 0) {
+        const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
+        const int row = row0 + r;
+        uint16_t* dst = p.out + int64_t(t0 + row / p.group) * p.out_stride +
+                        int64_t(head * p.group + row % p.group) * D + d;
+        *reinterpret_cast<uint2*>(dst) =
+            make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+      } else {
+        float* part = p.part + int64_t(dest) * (R * (D + 2));
+        *reinterpret_cast<float4*>(part + r * D + d) = o;
+        if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(top, sum);
+      }
+    }
+    __syncwarp();
+    if (lane == 0) mbar_arrive(&sh.taken);
+    ++merges;
+  }
+}
+
+constexpr int kJoinThreads = 128;
+constexpr int kJoinRows = 4;               // CTAs along y: rows r, r + 4, ...
+
+// Joins the parts of the item that starts in CTA blockIdx.x's run: parts
+// `slot`, then the first part of each CTA up to `last`, in that order.
+template <typename T, int D, int R>
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionParams p, int grid) {
+  constexpr int Q = D / 4;                 // threads along a row
+  constexpr int GR = kJoinThreads / Q;     // parts summed side by side
+  extern __shared__ float weight[];        // [grid]
+  __shared__ float4 sums[GR][Q];
+  __shared__ float red[2][kJoinThreads / 32];
+  pdl_launch();
+  pdl_wait();
+  const Join j = p.joins[blockIdx.x];
+  if (j.last < 0) return;
+  const int c0 = blockIdx.x, n = j.last - c0 + 1;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int64_t size = R * (D + 2);
+  for (int r = blockIdx.y; r < j.rows; r += kJoinRows) {
+    const float* base = p.part;
+    auto part = [&](int i) { return base + int64_t(i == 0 ? j.slot : 2 * (c0 + i)) * size; };
+    float top = -INFINITY;
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+      const float v = part(i)[R * D + 2 * r];
+      weight[i] = v;
+      top = fmaxf(top, v);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) red[0][warp] = top;
+    __syncthreads();
+    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
+    float sum = 0.0f;
+    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
+      const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[i] - top);
+      weight[i] = f;
+      sum = fmaf(f, part(i)[R * D + 2 * r + 1], sum);
+    }
+#pragma unroll
+    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    if (lane == 0) red[1][warp] = sum;
+    __syncthreads();
+    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
+    const int gr = threadIdx.x / Q, d = threadIdx.x % Q;
+    float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll 4
+    for (int i = gr; i < n; i += GR) {
+      const float4 x = *reinterpret_cast<const float4*>(part(i) + r * D + 4 * d);
+      const float f = weight[i];
+      o.x = fmaf(f, x.x, o.x);
+      o.y = fmaf(f, x.y, o.y);
+      o.z = fmaf(f, x.z, o.z);
+      o.w = fmaf(f, x.w, o.w);
+    }
+    sums[gr][d] = o;
+    __syncthreads();
+    if (gr == 0) {
+#pragma unroll
+      for (int i = 1; i < GR; ++i) {
+        const float4 x = sums[i][d];
+        o.x += x.x;
+        o.y += x.y;
+        o.z += x.z;
+        o.w += x.w;
+      }
+      const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
+      const int row = j.row0 + r;
+      uint16_t* dst = p.out + int64_t(j.t0 + row / p.group) * p.out_stride +
+                      int64_t(j.head * p.group + row % p.group) * D + 4 * d;
+      *reinterpret_cast<uint2*>(dst) =
+          make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+    }
+    __syncthreads();
+  }
+}
+
+// ---------------------------------------------------------------------------
+// host side
+// ---------------------------------------------------------------------------
+using DecodeFn = void (*)(CUtensorMap, CUtensorMap, AttentionParams);
+using JoinFn = void (*)(AttentionParams, int);
+
+struct Variant {
+  DecodeFn decode;
+  JoinFn join;
+  int R, smem;
+};
+
+template <typename T, int D, int FMT>
+Variant variant_of(int nt) {
+  if (nt == 1)
+    return {decode_attention_kernel<T, D, FMT, 1>, join_kernel<T, D, 8>, 8, int(sizeof(Shared<D, 8>)) + 1024};
+  return {decode_attention_kernel<T, D, FMT, 2>, join_kernel<T, D, 16>, 16, int(sizeof(Shared<D, 16>)) + 1024};
+}
+
+template <typename T>
+Variant variant_of(int d, int fmt, int nt) {
+  if (d == 128) return fmt == AWQ_KV_INT8 ? variant_of<T, 128, AWQ_KV_INT8>(nt) : variant_of<T, 128, AWQ_KV_E4M3>(nt);
+  return fmt == AWQ_KV_INT8 ? variant_of<T, 64, AWQ_KV_INT8>(nt) : variant_of<T, 64, AWQ_KV_E4M3>(nt);
+}
+
+// The kernel's shared memory limit raised and its resident CTAs counted, once
+// per kernel and device.
+awq_status_t resident(const Variant& v, int key, int* grid) {
+  constexpr int kDevices = 64;
+  static std::atomic<int> known[16][kDevices];
+  int dev = 0;
+  if (cudaGetDevice(&dev) != cudaSuccess) return AWQ_ERR_CUDA;
+  const bool keep = dev < kDevices;
+  int n = keep ? known[key][dev].load(std::memory_order_acquire) : 0;
+  if (n == 0) {
+    int sms = 0, per_sm = 0;
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(v.decode), cudaFuncAttributeMaxDynamicSharedMemorySize,
+                             v.smem) != cudaSuccess ||
+        cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(v.decode), kThreads,
+                                                      v.smem) != cudaSuccess ||
+        per_sm < 1) {
+      cudaGetLastError();
+      return AWQ_ERR_CUDA;
+    }
+    n = sms * per_sm;
+    if (keep) known[key][dev].store(n, std::memory_order_release);
+  }
+  *grid = n;
+  return AWQ_OK;
+}
+
+size_t workspace_of(const Variant& v, int grid, int d) {
+  return size_t(grid) * sizeof(Join) + size_t(grid) * 2 * v.R * (d + 2) * sizeof(float);
+}
+
+// Row tiles of 8 while the longest sequence's rows fit one; tiles of 16 read
+// the cache half as often beyond that.
+int row_tiles_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
+
+awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
+                             int32_t n_q_heads) {
+  awq_status_t st;
+  if ((st = check_cache(cache)) != AWQ_OK || (st = check_batch(batch, n_tokens)) != AWQ_OK ||
+      (st = check_capacity(cache, batch)) != AWQ_OK)
+    return st;
+  if (n_q_heads < 1 || n_q_heads > 65536 || n_q_heads % cache->n_kv_heads) return AWQ_ERR_SHAPE;
+  if (n_tokens * (n_q_heads / cache->n_kv_heads) > INT32_MAX / 2) return AWQ_ERR_SHAPE;
+  return AWQ_OK;
+}
+
+struct Plan {
+  Variant v;
+  int grid;
+};
+
+awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens, int32_t dtype,
+                     int32_t n_q_heads, Plan* plan) {
+  const int64_t most = batch->max_q_len > 0 && batch->max_q_len < n_tokens ? batch->max_q_len : n_tokens;
+  const int nt = row_tiles_of(most * (n_q_heads / cache->n_kv_heads));
+  plan->v = dtype == AWQ_KV_FP16 ? variant_of<__half>(cache->head_dim, cache->format, nt)
+                                 : variant_of<__nv_bfloat16>(cache->head_dim, cache->format, nt);
+  const int key = (dtype == AWQ_KV_BF16) * 8 + (cache->head_dim == 128) * 4 + (cache->format == AWQ_KV_E4M3) * 2 + nt - 1;
+  return resident(plan->v, key, &plan->grid);
+}
+
+}  // namespace
+
+awq_status_t attention_take_error(uint32_t* word, cudaStream_t s) {
+  const uint32_t zero = 0;
+  if (cudaMemcpyFromSymbolAsync(word, g_kv_attention_error, sizeof(uint32_t), 0, cudaMemcpyDeviceToHost, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess ||
+      cudaMemcpyToSymbolAsync(g_kv_attention_error, &zero, sizeof(uint32_t), 0, cudaMemcpyHostToDevice, s) !=
+          cudaSuccess ||
+      cudaStreamSynchronize(s) != cudaSuccess)
+    return AWQ_ERR_CUDA;
+  return AWQ_OK;
+}
+
+}  // namespace kv
+}  // namespace awq
+
+extern "C" awq_status_t awq_kv_attention_workspace_bytes(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch,
+                                                         int64_t n_tokens, int32_t n_q_heads, size_t* bytes) {
+  using namespace awq;
+  using namespace awq::kv;
+  if (!bytes) return AWQ_ERR_NULL;
+  awq_status_t st = check_attention(cache, batch, n_tokens, n_q_heads);
+  if (st != AWQ_OK) return st;
+  *bytes = 0;
+  if (n_tokens == 0 || batch->n_seqs == 0) return AWQ_OK;
+  for (int32_t dtype : {AWQ_KV_FP16, AWQ_KV_BF16}) {
+    Plan plan;
+    if ((st = plan_of(cache, batch, n_tokens, dtype, n_q_heads, &plan)) != AWQ_OK) return st;
+    const size_t need = workspace_of(plan.v, plan.grid, cache->head_dim);
+    if (need > *bytes) *bytes = need;
+  }
+  return AWQ_OK;
+}
+
+extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
+                                         int32_t dtype, const uint16_t* q, int64_t q_stride, int32_t n_q_heads,
+                                         float scale, int32_t window, int32_t sinks, uint16_t* out, int64_t out_stride,
+                                         void* workspace, size_t workspace_bytes, void* stream) {
+  using namespace awq;
+  using namespace awq::kv;
+  awq_status_t st = check_attention(cache, batch, n_tokens, n_q_heads);
+  if (st != AWQ_OK) return st;
+  if (!check_dtype(dtype)) return AWQ_ERR_UNSUPPORTED;
+  if (window < 0 || sinks < 0 || !(scale - scale == 0.0f)) return AWQ_ERR_SHAPE;
+  if (n_tokens == 0 || batch->n_seqs == 0) return AWQ_OK;
+  if ((st = check_pointers(cache, batch)) != AWQ_OK) return st;
+  if ((st = check_rows(q, q_stride, n_q_heads, cache->head_dim)) != AWQ_OK ||
+      (st = check_rows(out, out_stride, n_q_heads, cache->head_dim)) != AWQ_OK)
+    return st;
+  Plan plan;
+  if ((st = plan_of(cache, batch, n_tokens, dtype, n_q_heads, &plan)) != AWQ_OK) return st;
+  if (!workspace || workspace_bytes < workspace_of(plan.v, plan.grid, cache->head_dim)) return AWQ_ERR_WORKSPACE;
+  if (!aligned16(workspace)) return AWQ_ERR_ALIGN;
+
+  AttentionParams p = {};
+  p.batch = make_batch(cache, batch, n_tokens);
+  p.q = q;
+  p.out = out;
+  p.q_stride = q_stride;
+  p.out_stride = out_stride;
+  p.k_scales = cache->k_scales;
+  p.v_scales = cache->v_scales;
+  p.scale_stride = cache->scale_stride;
+  p.scale_log2 = scale * kLog2e;
+  p.window = window;
+  p.sinks = window ? sinks : 0;
+  p.group = n_q_heads / cache->n_kv_heads;
+  p.n_kv_heads = cache->n_kv_heads;
+  p.joins = static_cast<Join*>(workspace);
+  p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + size_t(plan.grid) * sizeof(Join));
+
+  // A page's tokens of one head are rows of head_dim bytes; a box is one scale block of them.
+  CUtensorMap map_k, map_v;
+  const uint64_t D = cache->head_dim;
+  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  // (an empty cache still gets a map: every page id is then out of range and no copy is issued)
+  const uint64_t pages = cache->n_pages > 0 ? cache->n_pages : 1;
+  if (!make_tensor_map_4d(&map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->k_pages, D, cache->page_size,
+                          cache->n_kv_heads, pages, D, D * cache->page_size, cache->page_stride, uint32_t(D), kBlock, 1,
+                          1, sw) ||
+      !make_tensor_map_4d(&map_v, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->v_pages, D, cache->page_size,
+                          cache->n_kv_heads, pages, D, D * cache->page_size, cache->page_stride, uint32_t(D), kBlock, 1,
+                          1, sw))
+    return AWQ_ERR_CUDA;
+
+  cudaLaunchAttribute attr;
+  cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), kThreads, plan.v.smem, stream, &attr);
+  if (cudaLaunchKernelEx(&lc, plan.v.decode, map_k, map_v, p) != cudaSuccess) {
+    cudaGetLastError();
+    return AWQ_ERR_CUDA;
+  }
+  lc = overlapped(dim3(unsigned(plan.grid), kJoinRows), kJoinThreads, plan.grid * sizeof(float), stream, &attr);
+  if (cudaLaunchKernelEx(&lc, plan.v.join, p, plan.grid) != cudaSuccess) {
+    cudaGetLastError();
+    return AWQ_ERR_CUDA;
+  }
+  return AWQ_OK;
+}
