@@ -218,6 +218,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   }
   pdl_launch();
   pdl_wait();
+  // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_sleep(bar, parity, abort, err, kErrWait)) != 0;
+  };
 
   // this CTA's run of units
   int64_t per = 0, total = 0, rest = 0;
@@ -301,7 +305,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       while (more) {
         more = u < u1;
         if (more) next(after);         // its page ids load while the current stage is issued
-        if (!wait_sleep(&sh.empty[s], ph ^ 1, abort, err, kErrWait)) {
+        if (!wait(&sh.empty[s], ph ^ 1)) {
           ok = false;
           break;
         }
@@ -364,7 +368,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   int s = 0;
   uint32_t ph = 0, merges = 0;
   for (int64_t u = u0; u < u1;) {
-    if (!wait_sleep(&sh.full[s], ph, abort, err, kErrWait)) return;
+    if (!wait(&sh.full[s], ph)) return;
     const auto& me = sh.meta[s];
     const int first = me.first, last = me.last, t0 = me.t0, row0 = me.row0, rows = me.rows, past = me.past,
               head = me.head, dest = me.dest, cnt = me.cnt, tile = me.tile[warp];
@@ -514,7 +518,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     if (!last) continue;
 
     // join the warps' parts of the item
-    if (merges && !wait_sleep(&sh.taken, (merges - 1) & 1, abort, err, kErrWait)) return;
+    if (merges && !wait(&sh.taken, (merges - 1) & 1)) return;
 #pragma unroll
     for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
@@ -537,7 +541,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.merged);
-    if (!wait_sleep(&sh.merged, merges & 1, abort, err, kErrWait)) return;
+    if (!wait(&sh.merged, merges & 1)) return;
     for (int i = threadIdx.x; i < rows * (D / 4); i += W * 32) {
       const int r = i / (D / 4), d = i % (D / 4) * 4;
       float top = -INFINITY;
@@ -651,46 +655,57 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
   }
 }
 
+#include "awq_kv_prefill.cuh"
+
 // ---------------------------------------------------------------------------
 // host side
 // ---------------------------------------------------------------------------
 using DecodeFn = void (*)(CUtensorMap, CUtensorMap, AttentionParams);
 using JoinFn = void (*)(AttentionParams, int);
+using JoinRowsFn = void (*)(AttentionParams);
 
+// kind 0, 1: up to 8 / 16 rows a tile; 2: pairs of row tiles of 128.
 struct Variant {
-  DecodeFn decode;
+  DecodeFn main;
   JoinFn join;
-  int R, smem;
+  JoinRowsFn join_rows;   // kind 2's
+  int R, smem, threads;
 };
 
 template <typename T, int D, int FMT>
-Variant variant_of(int nt) {
-  if (nt == 1)
-    return {decode_attention_kernel<T, D, FMT, 1>, join_kernel<T, D, 8>, 8, int(sizeof(Shared<D, 8>)) + 1024};
-  return {decode_attention_kernel<T, D, FMT, 2>, join_kernel<T, D, 16>, 16, int(sizeof(Shared<D, 16>)) + 1024};
+Variant variant_of(int kind) {
+  if (kind == 0)
+    return {decode_attention_kernel<T, D, FMT, 1>, join_kernel<T, D, 8>, nullptr, 8, int(sizeof(Shared<D, 8>)) + 1024,
+            kThreads};
+  if (kind == 1)
+    return {decode_attention_kernel<T, D, FMT, 2>, join_kernel<T, D, 16>, nullptr, 16,
+            int(sizeof(Shared<D, 16>)) + 1024, kThreads};
+  return {prefill_attention_kernel<T, D, FMT>, nullptr, join_rows_kernel<T, D>, kPairRows,
+          int(sizeof(PreShared<D>)) + 1024, kPreThreads};
 }
 
 template <typename T>
-Variant variant_of(int d, int fmt, int nt) {
-  if (d == 128) return fmt == AWQ_KV_INT8 ? variant_of<T, 128, AWQ_KV_INT8>(nt) : variant_of<T, 128, AWQ_KV_E4M3>(nt);
-  return fmt == AWQ_KV_INT8 ? variant_of<T, 64, AWQ_KV_INT8>(nt) : variant_of<T, 64, AWQ_KV_E4M3>(nt);
+Variant variant_of(int d, int fmt, int kind) {
+  if (d == 128)
+    return fmt == AWQ_KV_INT8 ? variant_of<T, 128, AWQ_KV_INT8>(kind) : variant_of<T, 128, AWQ_KV_E4M3>(kind);
+  return fmt == AWQ_KV_INT8 ? variant_of<T, 64, AWQ_KV_INT8>(kind) : variant_of<T, 64, AWQ_KV_E4M3>(kind);
 }
 
 // The kernel's shared memory limit raised and its resident CTAs counted, once
 // per kernel and device.
 awq_status_t resident(const Variant& v, int key, int* grid) {
   constexpr int kDevices = 64;
-  static std::atomic<int> known[16][kDevices];
+  static std::atomic<int> known[24][kDevices];
   int dev = 0;
   if (cudaGetDevice(&dev) != cudaSuccess) return AWQ_ERR_CUDA;
   const bool keep = dev < kDevices;
   int n = keep ? known[key][dev].load(std::memory_order_acquire) : 0;
   if (n == 0) {
     int sms = 0, per_sm = 0;
-    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(v.decode), cudaFuncAttributeMaxDynamicSharedMemorySize,
+    if (cudaFuncSetAttribute(reinterpret_cast<const void*>(v.main), cudaFuncAttributeMaxDynamicSharedMemorySize,
                              v.smem) != cudaSuccess ||
         cudaDeviceGetAttribute(&sms, cudaDevAttrMultiProcessorCount, dev) != cudaSuccess ||
-        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(v.decode), kThreads,
+        cudaOccupancyMaxActiveBlocksPerMultiprocessor(&per_sm, reinterpret_cast<const void*>(v.main), v.threads,
                                                       v.smem) != cudaSuccess ||
         per_sm < 1) {
       cudaGetLastError();
@@ -707,9 +722,9 @@ size_t workspace_of(const Variant& v, int grid, int d) {
   return size_t(grid) * sizeof(Join) + size_t(grid) * 2 * v.R * (d + 2) * sizeof(float);
 }
 
-// Row tiles of 8 while the longest sequence's rows fit one; tiles of 16 read
-// the cache half as often beyond that.
-int row_tiles_of(int64_t rows) { return rows <= 8 ? 1 : 2; }
+// By the rows (tokens x group) of the longest sequence: tiles of 8 while they
+// fit one, of 16 while they fit that, else pairs of 128.
+int kind_of(int64_t rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : 2; }
 
 awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
                              int32_t n_q_heads) {
@@ -730,10 +745,10 @@ struct Plan {
 awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens, int32_t dtype,
                      int32_t n_q_heads, Plan* plan) {
   const int64_t most = batch->max_q_len > 0 && batch->max_q_len < n_tokens ? batch->max_q_len : n_tokens;
-  const int nt = row_tiles_of(most * (n_q_heads / cache->n_kv_heads));
-  plan->v = dtype == AWQ_KV_FP16 ? variant_of<__half>(cache->head_dim, cache->format, nt)
-                                 : variant_of<__nv_bfloat16>(cache->head_dim, cache->format, nt);
-  const int key = (dtype == AWQ_KV_BF16) * 8 + (cache->head_dim == 128) * 4 + (cache->format == AWQ_KV_E4M3) * 2 + nt - 1;
+  const int kind = kind_of(most * (n_q_heads / cache->n_kv_heads));
+  plan->v = dtype == AWQ_KV_FP16 ? variant_of<__half>(cache->head_dim, cache->format, kind)
+                                 : variant_of<__nv_bfloat16>(cache->head_dim, cache->format, kind);
+  const int key = (((dtype == AWQ_KV_BF16) * 2 + (cache->head_dim == 128)) * 2 + (cache->format == AWQ_KV_E4M3)) * 3 + kind;
   return resident(plan->v, key, &plan->grid);
 }
 
@@ -812,7 +827,10 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   // A page's tokens of one head are rows of head_dim bytes; a box is one scale block of them.
   CUtensorMap map_k, map_v;
   const uint64_t D = cache->head_dim;
-  const CUtensorMapSwizzle sw = D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B : CU_TENSOR_MAP_SWIZZLE_64B;
+  const bool many = plan.v.join_rows != nullptr;
+  const CUtensorMapSwizzle sw = many       ? CU_TENSOR_MAP_SWIZZLE_NONE
+                                : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
+                                           : CU_TENSOR_MAP_SWIZZLE_64B;
   // (an empty cache still gets a map: every page id is then out of range and no copy is issued)
   const uint64_t pages = cache->n_pages > 0 ? cache->n_pages : 1;
   if (!make_tensor_map_4d(&map_k, CU_TENSOR_MAP_DATA_TYPE_UINT8, cache->k_pages, D, cache->page_size,
@@ -824,13 +842,16 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
     return AWQ_ERR_CUDA;
 
   cudaLaunchAttribute attr;
-  cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), kThreads, plan.v.smem, stream, &attr);
-  if (cudaLaunchKernelEx(&lc, plan.v.decode, map_k, map_v, p) != cudaSuccess) {
-    cudaGetLastError();
-    return AWQ_ERR_CUDA;
+  cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), plan.v.threads, plan.v.smem, stream, &attr);
+  cudaError_t e = cudaLaunchKernelEx(&lc, plan.v.main, map_k, map_v, p);
+  if (e == cudaSuccess && many) {
+    lc = overlapped(dim3(unsigned(plan.grid), kPairRows / 8), 256, 0, stream, &attr);
+    e = cudaLaunchKernelEx(&lc, plan.v.join_rows, p);
+  } else if (e == cudaSuccess) {
+    lc = overlapped(dim3(unsigned(plan.grid), kJoinRows), kJoinThreads, plan.grid * sizeof(float), stream, &attr);
+    e = cudaLaunchKernelEx(&lc, plan.v.join, p, plan.grid);
   }
-  lc = overlapped(dim3(unsigned(plan.grid), kJoinRows), kJoinThreads, plan.grid * sizeof(float), stream, &attr);
-  if (cudaLaunchKernelEx(&lc, plan.v.join, p, plan.grid) != cudaSuccess) {
+  if (e != cudaSuccess) {
     cudaGetLastError();
     return AWQ_ERR_CUDA;
   }

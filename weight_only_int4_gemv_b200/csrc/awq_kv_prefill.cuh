@@ -1,0 +1,827 @@
+// The many-row kernel of awq_kv_attention (prompts, chunks of prompts),
+// included by awq_kv_attention.cu inside namespace awq::kv.
+//
+// Mathematics: as for few rows (t = scale log2(e) s_k S + log2(s_v), p = 2^(t
+// - m), y = sum p c_v / sum (p / s_v)), over tiles of 128 rows by 128 keys.
+//
+// What bounds it: two products of 128 x 128 x head_dim and 128 x 128
+// exponentials per tile, about equal at the tensor and the special-function
+// units' rates; so both products run on tcgen05 and everything else is kept
+// off the warps that do the softmax. One CTA per SM takes two row tiles (256
+// rows of one key / value head: the rows of 256 / group tokens) against the
+// same keys, so a code is turned into its fp16 form once for two products,
+// and the softmax of one row tile runs while the other's products do.
+//
+// Warps:
+//   0-3, 4-7  softmax of row tile 0 / 1: one row per thread. S comes from
+//             tensor memory, the weights go back over it as fp16 (the A
+//             operand of the second product). m is only raised when a logit
+//             passes it by more than 8 (log2 units), so the outputs in tensor
+//             memory are almost never rescaled and a tile needs one pass.
+//   8-11      codes to fp16 (exact) in the tensor core's 128-byte-swizzled
+//             layout: keys K-major, values as they lie (MN-major); q rows.
+//   12        pages, scales and the tiles' descriptions, TMA of the codes.
+//   13        the products: S0 = Q0 K^T, S1 = Q1 K^T, O0 += P0 V, O1 += P1 V.
+// Tensor memory: S0, S1 (128 columns each; P lies over its S), O0, O1.
+//
+// Work is laid end to end in units of 128 keys and cut evenly over the CTAs,
+// as for few rows; split items meet in join_rows_kernel.
+
+constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
+constexpr int kPairRows = 2 * kTile;
+constexpr int kPreThreads = 14 * 32;
+constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
+
+enum : int {                                   // PreMeta::flags
+  kAct0 = 1, kAct1 = 2,                        // the row tile sees some of these keys
+  kBegin = 4, kEnd = 8,                        // first / last tile of the segment
+  kBegin0 = 16, kBegin1 = 32,                  // the row tile's first tile of the segment
+  kEnd0 = 64, kEnd1 = 128,                     // its last
+  kHas0 = 256, kHas1 = 512,                    // the row tile has a tile in the segment
+  kStop = 1024                                 // no more tiles
+};
+
+struct PreMeta {
+  int pos, valid, flags;
+  int t0, row0, rows, past, head, dest;
+  int pad[3];
+  float ks[8], vs[8];
+};
+
+template <int D>
+struct PreShared {
+  uint8_t q[2][kTile * D * 2];
+  uint8_t half[kHalfSlots][kTile * D * 2];
+  uint8_t raw[kRawSlots][kTile * D];
+  float factor[kMetaSlots][2][kTile];          // [segment][row tile][row]: a ring of as many segments as tiles
+  PreMeta meta[kMetaSlots];
+  uint64_t meta_full[kMetaSlots], meta_empty[kMetaSlots];
+  uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
+  uint64_t half_full[kHalfSlots], half_empty[kHalfSlots];
+  uint64_t q_full[2], q_free[2], s_full[2], p_ready[2], o_full[2], o_free[2], done;
+  uint32_t tmem;
+  int abort;
+};
+
+__device__ __forceinline__ void tc_before() { asm volatile("tcgen05.fence::before_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_after() { asm volatile("tcgen05.fence::after_thread_sync;" ::: "memory"); }
+__device__ __forceinline__ void tc_commit(uint64_t* bar) {
+  asm volatile("tcgen05.commit.cta_group::1.mbarrier::arrive::one.shared::cluster.b64 [%0];" ::"r"(smem_u32(bar))
+               : "memory");
+}
+// D += A B, both operands in shared memory
+__device__ __forceinline__ void tc_mma_ss(uint32_t d, uint64_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], %1, %2, %3, p;\n\t}" ::"r"(d), "l"(a), "l"(b), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+// D += A B, A in tensor memory
+__device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, uint32_t idesc, uint32_t accumulate) {
+  asm volatile(
+      "{\n\t.reg .pred p;\n\tsetp.ne.b32 p, %4, 0;\n\t"
+      "tcgen05.mma.cta_group::1.kind::f16 [%0], [%1], %2, %3, p;\n\t}" ::"r"(d), "r"(a), "l"(b), "r"(idesc),
+      "r"(accumulate)
+      : "memory");
+}
+// this warp's 32 lanes x 32 columns (with the wait in the same statement: nothing may read r before it)
+__device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+        "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
+        "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
+        "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+      : "r"(a)
+      : "memory");
+}
+__device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x32.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,"
+      "%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31,%32};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15]), "r"(r[16]), "r"(r[17]), "r"(r[18]),
+      "r"(r[19]), "r"(r[20]), "r"(r[21]), "r"(r[22]), "r"(r[23]), "r"(r[24]), "r"(r[25]), "r"(r[26]), "r"(r[27]),
+      "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
+      : "memory");
+}
+__device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
+
+// Shared-memory operand descriptors, 128-byte swizzle. K-major: 8-row groups
+// 1024 bytes apart. MN-major (values: rows are keys, 64 channels a panel):
+// panels kTile rows apart, 8-key groups 1024 bytes apart.
+__device__ __forceinline__ uint64_t desc_k(uint32_t a) {
+  return uint64_t((a >> 4) & 0x3FFF) | (uint64_t(1) << 16) | (uint64_t(1024 >> 4) << 32) | (uint64_t(1) << 46) |
+         (uint64_t(2) << 61);
+}
+__device__ __forceinline__ uint64_t desc_mn(uint32_t a) {
+  return uint64_t((a >> 4) & 0x3FFF) | (uint64_t(kTile * 128 >> 4) << 16) | (uint64_t(1024 >> 4) << 32) |
+         (uint64_t(1) << 46) | (uint64_t(2) << 61);
+}
+
+// One row pair: rows row0 .. of a sequence, the tiles each half sees, and
+// their union (sink tiles, then tiles from w0).
+struct Pair {
+  int hi[2], lo[2];      // last (-1: none) and first window tile of each half
+  int sink_tiles, w0, tiles;
+};
+
+__device__ __forceinline__ Pair pair_of(const AttentionParams& p, const Seq& s, int row0) {
+  Pair r;
+  const int rows = s.n * p.group;
+  int hi = -1, lo = 1 << 30, low = 0;
+#pragma unroll
+  for (int x = 0; x < 2; ++x) {
+    r.hi[x] = -1;
+    r.lo[x] = 0;
+    const int first = row0 + x * kTile;
+    if (first < rows) {
+      const int p_low = s.past + first / p.group, p_high = s.past + (min(first + kTile, rows) - 1) / p.group;
+      if (p_high >= 0) {
+        r.hi[x] = p_high / kTile;
+        const int start = p.window ? max(0, p_low - p.window + 1) : 0;
+        r.lo[x] = start / kTile;
+        if (x == 0 || hi < 0) low = start;
+        hi = max(hi, r.hi[x]);
+        lo = min(lo, r.lo[x]);
+      }
+    }
+  }
+  if (hi < 0) {          // rows that see nothing: one tile without keys, for their zeros
+    r.sink_tiles = r.w0 = 0;
+    r.tiles = 1;
+    return r;
+  }
+  r.w0 = lo;
+  r.sink_tiles = p.window ? min((min(p.sinks, low) + kTile - 1) / kTile, lo) : 0;
+  r.tiles = r.sink_tiles + hi - lo + 1;
+  return r;
+}
+
+// Units of a sequence (all lanes of a warp together).
+__device__ __forceinline__ int64_t pair_units(const AttentionParams& p, const Seq& s, int lane) {
+  const int pairs = (s.n * p.group + kPairRows - 1) / kPairRows;
+  int64_t sum = 0;
+  for (int i = lane; i < pairs; i += 32) sum += pair_of(p, s, i * kPairRows).tiles;
+#pragma unroll
+  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+  return sum * p.n_kv_heads;
+}
+
+// 16 raw codes to 16 fp16 numbers, two 16-byte chunks.
+template <int FMT>
+__device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
+  a = make_uint4(code_pair<FMT, 0>(c.x), code_pair<FMT, 2>(c.x), code_pair<FMT, 0>(c.y), code_pair<FMT, 2>(c.y));
+  b = make_uint4(code_pair<FMT, 0>(c.z), code_pair<FMT, 2>(c.z), code_pair<FMT, 0>(c.w), code_pair<FMT, 2>(c.w));
+}
+
+template <typename T, int D, int FMT>
+__global__ void __launch_bounds__(kPreThreads, 1)
+prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
+                         const __grid_constant__ AttentionParams p) {
+  using Sh = PreShared<D>;
+  constexpr int kPanels = D / 64;
+  constexpr int kRawBytes = kTile * D;
+  constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kTile >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+  constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
+  extern __shared__ uint8_t smem_raw[];
+  Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  volatile int* abort = &sh.abort;
+  uint32_t* err = &g_kv_attention_error;
+  if (threadIdx.x == 0) {
+    for (int i = 0; i < kMetaSlots; ++i) {
+      mbar_init(&sh.meta_full[i], 33);
+      mbar_init(&sh.meta_empty[i], 13);        // 8 softmax and 4 converting warps, the products' thread
+    }
+    for (int i = 0; i < kRawSlots; ++i) {
+      mbar_init(&sh.raw_full[i], 1);
+      mbar_init(&sh.raw_empty[i], 4);
+    }
+    for (int i = 0; i < kHalfSlots; ++i) {
+      mbar_init(&sh.half_full[i], 4);
+      mbar_init(&sh.half_empty[i], 1);
+    }
+    for (int x = 0; x < 2; ++x) {
+      mbar_init(&sh.q_full[x], 4);
+      mbar_init(&sh.q_free[x], 1);
+      mbar_init(&sh.s_full[x], 1);
+      mbar_init(&sh.p_ready[x], 4);
+      mbar_init(&sh.o_full[x], 1);
+      mbar_init(&sh.o_free[x], 4);
+    }
+    mbar_init(&sh.done, 1);
+    sh.abort = 0;
+    asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
+    fence_proxy_async_smem();
+  }
+  if (warp == 13) {
+    asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)));
+    asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
+  }
+  tc_before();
+  pdl_launch();
+  pdl_wait();
+  __syncthreads();
+  tc_after();
+  const uint32_t tmem = sh.tmem;
+  // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
+  auto wait = [&](uint64_t* bar, uint32_t parity) {
+    return __all_sync(0xffffffffu, wait_sleep(bar, parity, abort, err, kErrWait)) != 0;
+  };
+
+  if (warp < 8) {
+    // -------------------------------------------------------------- softmax
+    const int x = warp >> 2, row = threadIdx.x & (kTile - 1);
+    const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
+    const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 2 * kTile + x * D;
+    float m = -INFINITY, l = 0.0f, factor = 0.0f;
+    int pv = 0, p_row = 0, p_low = 0, p_high = 0;      // pv: products into O in this segment
+    uint32_t s_ph = 0, o_ph = 0;                       // parity of the next S, of the next O
+    uint32_t seg = 0;
+    for (int it = 0;; ++it) {
+      const int mi = it % kMetaSlots;
+      if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) break;
+      const PreMeta& me = sh.meta[mi];
+      const int flags = me.flags;
+      if (flags & kStop) break;
+      if (flags & kBegin) {
+        m = -INFINITY;
+        l = 0.0f;
+        pv = 0;
+        const int r0 = me.row0 + x * kTile, r1 = min(r0 + kTile, me.row0 + me.rows) - 1;
+        p_low = me.past + r0 / p.group;
+        p_high = me.past + r1 / p.group;
+        p_row = me.past + (r0 + row) / p.group;
+      }
+      if (flags & (x ? kAct1 : kAct0)) {
+        if (!wait(&sh.s_full[x], s_ph)) break;
+        s_ph ^= 1;
+        tc_after();
+        if (pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];   // written before S was computed
+        const int pos = me.pos;
+        const bool all = pos + kTile - 1 <= p_low &&
+                         (p.window == 0 || pos > p_high - p.window || pos + kTile <= p.sinks);
+        const int hi = p_row - pos, lo = p.window ? hi - p.window + 1 : 0, sk = p.window ? p.sinks - pos : 0;
+        uint32_t pk[kTile / 2];
+        float top, sum;
+        // weights of the row against m; top is the largest logit above m
+        auto weigh = [&](auto masked, auto weights) {
+          const float base = m == -INFINITY ? 0.0f : m;
+          top = -INFINITY;
+          sum = 0.0f;
+#pragma unroll
+          for (int c = 0; c < kTile / 32; ++c) {
+            uint32_t r[32];
+            tc_ld32(ts + c * 32, r);
+#pragma unroll
+            for (int h = 0; h < 2; ++h) {
+              const float vs = me.vs[2 * c + h];
+              const float a = factor * me.ks[2 * c + h], b = __log2f(vs) - base, iv = __fdividef(1.0f, vs);
+              float part = 0.0f;
+#pragma unroll
+              for (int e = 0; e < 16; e += 2) {
+                float t[2];
+#pragma unroll
+                for (int f = 0; f < 2; ++f) {
+                  const int j = 32 * c + 16 * h + e + f;
+                  t[f] = fmaf(__uint_as_float(r[16 * h + e + f]), a, b);
+                  if (decltype(masked)::value && !(j <= hi && (j >= lo || j < sk))) t[f] = -INFINITY;
+                  top = fmaxf(top, t[f]);
+                }
+                if (decltype(weights)::value) {
+                  const float w0 = exp2_fast(t[0]), w1 = exp2_fast(t[1]);
+                  part += w0 + w1;
+                  pk[16 * c + 8 * h + e / 2] = Half16<__half>::pack(w0, w1);
+                }
+              }
+              if (decltype(weights)::value) sum = fmaf(part, iv, sum);
+            }
+          }
+          top += base;
+        };
+        auto pass = [&](auto weights) {
+          if (all)
+            weigh(std::false_type{}, weights);
+          else
+            weigh(std::true_type{}, weights);
+        };
+        bool again = true;
+        if (pv > 0) {
+          pass(std::true_type{});
+          again = __any_sync(0xffffffffu, top > m + kSlack);
+        } else {
+          pass(std::false_type{});
+        }
+        if (again) {
+          const float raised = fmaxf(m, top);
+          const float f = raised == -INFINITY ? 1.0f : exp2_fast(m - raised);
+          if (pv > 0) {
+            // the products so far are in, and are brought to the new maximum
+            if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
+            tc_after();
+#pragma unroll 1
+            for (int c = 0; c < D / 32; ++c) {
+              uint32_t r[32];
+              tc_ld32(to + c * 32, r);
+#pragma unroll
+              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
+              tc_st32(to + c * 32, r);
+            }
+          }
+          l *= f;
+          m = raised;
+          pass(std::true_type{});
+        }
+        l += sum;
+        tc_st32(ts, pk);
+        tc_st32(ts + 32, pk + 32);
+        tc_wait_st();
+        tc_before();
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.p_ready[x]);
+        ++pv;
+        o_ph ^= 1;
+      }
+      if (flags & kEnd) {
+        const int r0 = x * kTile + row;
+        const bool mine = r0 < me.rows;
+        const int gr = me.row0 + r0, dest = me.dest;
+        uint16_t* dst = p.out + int64_t(me.t0 + gr / p.group) * p.out_stride +
+                        int64_t(me.head * p.group + gr % p.group) * D;
+        float* part = p.part + int64_t(dest) * (kPairRows * (D + 2));
+        if (pv > 0) {
+          if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
+          tc_after();
+        }
+        const float inv = m == -INFINITY ? 0.0f : __fdiv_rn(1.0f, l);
+#pragma unroll 1
+        for (int c = 0; c < D / 32; ++c) {
+          uint32_t r[32];
+          if (pv > 0) {
+            tc_ld32(to + c * 32, r);
+          } else {
+#pragma unroll
+            for (int e = 0; e < 32; ++e) r[e] = 0;
+          }
+          if (mine && dest < 0) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 8) {
+              float v[8];
+#pragma unroll
+              for (int f = 0; f < 8; ++f) v[f] = __uint_as_float(r[e + f]) * inv;
+              *reinterpret_cast<uint4*>(dst + c * 32 + e) = pack8<T>(v);
+            }
+          } else if (mine) {
+#pragma unroll
+            for (int e = 0; e < 32; e += 4)
+              *reinterpret_cast<uint4*>(part + r0 * D + c * 32 + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+          }
+        }
+        if (mine && dest >= 0) *reinterpret_cast<float2*>(part + kPairRows * D + 2 * r0) = make_float2(m, l);
+        if (pv > 0) {
+          tc_before();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.o_free[x]);
+        }
+        ++seg;
+      }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+    }
+  } else if (warp < 12) {
+    // ----------------------------------------------- codes and q rows to fp16
+    const int tid = threadIdx.x - 8 * 32;
+    uint32_t q_ph[2] = {0, 0}, seg = 0;
+    int used[2] = {0, 0};
+    int n = 0;                                  // tiles of codes converted
+    for (int it = 0;; ++it) {
+      const int mi = it % kMetaSlots;
+      if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) break;
+      const PreMeta& me = sh.meta[mi];
+      const int flags = me.flags, valid = me.valid;
+      if (flags & kStop) break;
+      bool ok = true;
+      if (flags & kBegin) {
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(flags & (x ? kHas1 : kHas0))) continue;
+          // the row from memory while the buffer's last products finish
+          const int r = x * kTile + tid, gr = me.row0 + r;
+          uint4 v[D / 8];
+          const uint16_t* src = p.q + int64_t(me.t0 + gr / p.group) * p.q_stride +
+                                int64_t(me.head * p.group + gr % p.group) * D;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            v[i] = r < me.rows ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
+          float f = 1.0f;
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+            float top = 0.0f;
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              float y[8];
+              unpack8<T>(v[i], y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+            }
+            const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+            f = __uint_as_float(e << 23);
+            const float inv = __uint_as_float((254u - e) << 23);
+#pragma unroll
+            for (int i = 0; i < D / 8; ++i) {
+              float y[8];
+              unpack8<T>(v[i], y);
+#pragma unroll
+              for (int j = 0; j < 8; ++j) y[j] *= inv;
+              v[i] = pack8<__half>(y);
+            }
+          }
+          if (used[x]++) {
+            if (!wait(&sh.q_free[x], q_ph[x])) {
+              ok = false;
+              break;
+            }
+            q_ph[x] ^= 1;
+          }
+          uint8_t* dst = sh.q[x] + tid * 128;
+#pragma unroll
+          for (int i = 0; i < D / 8; ++i)
+            *reinterpret_cast<uint4*>(dst + (i >> 3) * (kTile * 128) + (((i & 7) ^ (tid & 7)) << 4)) = v[i];
+          sh.factor[seg % kMetaSlots][x][tid] = f;
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full[x]);
+        }
+      }
+      if (flags & kEnd) ++seg;
+      if (!ok) break;
+      if (!(flags & (kAct0 | kAct1))) {         // a tile without keys
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+        continue;
+      }
+      for (int kv = 0; kv < 2; ++kv, ++n) {
+        const int rs = n % kRawSlots, hs = n % kHalfSlots;
+        if (!wait(&sh.raw_full[rs], (n / kRawSlots) & 1) || !wait(&sh.half_empty[hs], ((n / kHalfSlots) & 1) ^ 1)) {
+          ok = false;
+          break;
+        }
+        constexpr int CPR = D / 16;             // raw 16-byte chunks of a key
+        const uint8_t* raw = sh.raw[rs];
+        uint8_t* out = sh.half[hs];
+#pragma unroll
+        for (int i = 0; i < kTile * CPR / 128; ++i) {
+          const int c = i * 128 + tid, r = c / CPR, k = c % CPR;
+          uint4 w = *reinterpret_cast<const uint4*>(raw + c * 16);
+          // e4m3 bytes behind the end may be NaN, which a weight of 0 does not silence
+          if (FMT == AWQ_KV_E4M3 && r >= valid) w = make_uint4(0, 0, 0, 0);
+          uint4 a, b;
+          widen16<FMT>(w, a, b);
+          // chunks 2k', 2k'+1 of the row's panel; the second panel's odd one first, so that a row's writes
+          // fall on different banks
+          uint8_t* dst = out + (k >> 2) * (kTile * 128) + r * 128;
+          const int odd = k >> 2;
+          const int c0 = 2 * (k & 3) + odd, c1 = 2 * (k & 3) + 1 - odd;
+          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = odd ? b : a;
+          *reinterpret_cast<uint4*>(dst + ((c1 ^ (r & 7)) << 4)) = odd ? a : b;
+        }
+        fence_proxy_async_smem();
+        __syncwarp();
+        if (lane == 0) {
+          mbar_arrive(&sh.half_full[hs]);
+          mbar_arrive(&sh.raw_empty[rs]);
+        }
+      }
+      if (!ok) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+    }
+  } else if (warp == 12) {
+    // --------------------------------------------- the schedule, pages, copies
+    int64_t total = 0;
+    const Batch& a = p.batch;
+    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
+      Seq mine = {0, 0, 0, 0};
+      if (b0 + lane < a.n_seqs) mine = load_seq(a, b0 + lane, err);
+      for (int i = 0; i < min(32, a.n_seqs - b0); ++i) {
+        const Seq s = {__shfl_sync(0xffffffffu, mine.t0, i), __shfl_sync(0xffffffffu, mine.n, i),
+                       __shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.past, i)};
+        total += pair_units(p, s, lane);
+      }
+    }
+    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
+    const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
+    Join join;
+    join.last = -1;
+    int it = 0, n = 0;
+    bool ok = true;
+    int64_t u = 0;                               // units before the sequence
+    for (int b0 = 0; b0 < a.n_seqs && u < u1 && ok; b0 += 32) {
+      Seq mine = {0, 0, 0, 0};
+      if (b0 + lane < a.n_seqs) mine = load_seq(a, b0 + lane, err);
+      for (int i = 0; i < min(32, a.n_seqs - b0) && u < u1 && ok; ++i) {
+        const Seq s = {__shfl_sync(0xffffffffu, mine.t0, i), __shfl_sync(0xffffffffu, mine.n, i),
+                       __shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.past, i)};
+        const int64_t units = pair_units(p, s, lane);
+        if (u + units <= u0) {
+          u += units;
+          continue;
+        }
+        const int32_t* table = a.table + int64_t(b0 + i) * a.table_stride;
+        const int rows = s.n * p.group, pairs = (rows + kPairRows - 1) / kPairRows;
+        int64_t begin = u;                       // units before the pair
+        u += units;
+        int start = 0;                           // the pair that holds unit u0, 32 looked at together
+        while (start < pairs) {
+          int inc = start + lane < pairs ? pair_of(p, s, (start + lane) * kPairRows).tiles : 0;
+          const int own = inc;
+#pragma unroll
+          for (int o = 1; o < 32; o <<= 1) {
+            const int y = __shfl_up_sync(0xffffffffu, inc, o);
+            if (lane >= o) inc += y;
+          }
+          const unsigned past = __ballot_sync(0xffffffffu, begin + int64_t(inc) * p.n_kv_heads > u0);
+          if (past) {
+            const int f = __ffs(past) - 1;
+            begin += int64_t(__shfl_sync(0xffffffffu, inc - own, f)) * p.n_kv_heads;
+            start += f;
+            break;
+          }
+          begin += int64_t(__shfl_sync(0xffffffffu, inc, 31)) * p.n_kv_heads;
+          start += 32;
+        }
+        for (int pr = start; pr < pairs && begin < u1 && ok; ++pr) {
+          const Pair pa = pair_of(p, s, pr * kPairRows);
+          const int64_t width = int64_t(pa.tiles) * p.n_kv_heads;
+          int head = u0 > begin ? int((u0 - begin) / pa.tiles) : 0;
+          for (; head < p.n_kv_heads && begin + int64_t(head) * pa.tiles < u1 && ok; ++head) {
+            const int64_t first = begin + int64_t(head) * pa.tiles, end = first + pa.tiles;
+            const int v0 = int(max(u0 - first, int64_t(0))), v1 = int(min(u1 - first, int64_t(pa.tiles)));
+            const bool whole = first >= u0 && end <= u1;
+            const int dest = whole ? -1 : int(2 * blockIdx.x) + (first > u0);
+            if (first >= u0 && end > u1) {
+              join.last = int((end - 1) / per);
+              join.slot = dest;
+              join.t0 = s.t0;
+              join.row0 = pr * kPairRows;
+              join.rows = min(kPairRows, rows - join.row0);
+              join.head = head;
+            }
+            // each half's first and last tile of the segment
+            int lo[2] = {INT32_MAX, INT32_MAX}, hi[2] = {-1, -1};
+            auto tile_of = [&](int v) { return v < pa.sink_tiles ? v : v - pa.sink_tiles + pa.w0; };
+            auto sees = [&](int x, int v) {
+              const int t = tile_of(v);
+              return t <= pa.hi[x] && (t >= pa.lo[x] || int64_t(t) * kTile < p.sinks);
+            };
+            for (int x = 0; x < 2; ++x) {
+              for (int v = v0 + lane; v < v1; v += 32)
+                if (sees(x, v)) {
+                  lo[x] = min(lo[x], v);
+                  hi[x] = max(hi[x], v);
+                }
+              lo[x] = __reduce_min_sync(0xffffffffu, lo[x]);
+              hi[x] = __reduce_max_sync(0xffffffffu, hi[x]);
+            }
+            for (int v = v0; v < v1; ++v, ++it) {
+              const int mi = it % kMetaSlots, pos = tile_of(v) * kTile;
+              int flags = (v == v0 ? kBegin : 0) | (v == v1 - 1 ? kEnd : 0);
+              for (int x = 0; x < 2; ++x) {
+                if (hi[x] >= 0) flags |= x ? kHas1 : kHas0;
+                if (sees(x, v)) flags |= x ? kAct1 : kAct0;
+                if (v == lo[x]) flags |= x ? kBegin1 : kBegin0;
+                if (v == hi[x]) flags |= x ? kEnd1 : kEnd0;
+              }
+              const bool keys = flags & (kAct0 | kAct1);
+              // lane i: block i of the keys, lane 8 + i: of the values
+              const int blk = pos + (lane & 7) * kBlock;
+              int page = -1;
+              if (keys && lane < 16 && blk < s.len) page = checked_page(a, table[blk / a.page_size], err);
+              const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
+              if (!wait(&sh.meta_empty[mi], ((it / kMetaSlots) & 1) ^ 1)) {
+                ok = false;
+                break;
+              }
+              PreMeta& me = sh.meta[mi];
+              const int off = blk % a.page_size;
+              if (lane < 16) {
+                float* dst = lane < 8 ? &me.ks[lane] : &me.vs[lane & 7];
+                if (page >= 0) {
+                  const float* sc = (lane < 8 ? p.k_scales : p.v_scales) + int64_t(page) * p.scale_stride +
+                                    head * (a.page_size / kBlock) + off / kBlock;
+                  asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(dst)), "l"(sc) : "memory");
+                } else {
+                  *dst = 1.0f;
+                }
+              }
+              asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.meta_full[mi]))
+                           : "memory");
+              if (lane == 0) {
+                me.pos = pos;
+                me.valid = min(kTile, s.len - pos);
+                me.flags = flags;
+                me.t0 = s.t0;
+                me.row0 = pr * kPairRows;
+                me.rows = min(kPairRows, rows - me.row0);
+                me.past = s.past;
+                me.head = head;
+                me.dest = dest;
+              }
+              __syncwarp();
+              if (lane == 0) mbar_arrive(&sh.meta_full[mi]);
+              if (!keys) continue;
+              for (int kv = 0; kv < 2; ++kv, ++n) {
+                const int rs = n % kRawSlots;
+                if (!wait(&sh.raw_empty[rs], ((n / kRawSlots) & 1) ^ 1)) {
+                  ok = false;
+                  break;
+                }
+                if (lane == 0) mbar_arrive_expect_tx(&sh.raw_full[rs], __popc(here & (kv ? 0xff00u : 0xffu)) * kBlock * D);
+                __syncwarp();
+                if (page >= 0 && (lane >> 3) == kv)
+                  tma_load_4d(sh.raw[rs] + (lane & 7) * kBlock * D, kv ? &map_v : &map_k, 0, off, head, page,
+                              &sh.raw_full[rs]);
+              }
+              if (!ok) break;
+            }
+          }
+          begin += width;
+        }
+      }
+    }
+    if (lane == 0) p.joins[blockIdx.x] = join;
+    if (ok) {
+      const int mi = it % kMetaSlots;
+      if (wait(&sh.meta_empty[mi], ((it / kMetaSlots) & 1) ^ 1)) {
+        asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.meta_full[mi]))
+                     : "memory");
+        if (lane == 0) {
+          sh.meta[mi].flags = kStop;
+          mbar_arrive(&sh.meta_full[mi]);
+        }
+      }
+    }
+    // every copy issued has landed before the CTA's shared memory goes
+    for (int i = max(0, n - kRawSlots); i < n; ++i)
+      wait_sleep_teardown(&sh.raw_full[i % kRawSlots], (i / kRawSlots) & 1);
+  } else if (lane == 0) {
+    // ----------------------------------------------------------- the products
+    // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
+    // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
+    auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_sleep(bar, parity, abort, err, kErrWait); };
+    uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, of_ph[2] = {0, 0};
+    int segs[2] = {0, 0};                        // segments the row tile's O was used in
+    int n = 0;                                   // code tiles taken
+    const uint32_t s_t[2] = {tmem, tmem + kTile}, o_t[2] = {tmem + 2 * kTile, tmem + 2 * kTile + D};
+    bool ok = true;
+    // S = Q K^T of row tile x
+    auto product_s = [&](int x, int hs, int flags) {
+      if (flags & (x ? kBegin1 : kBegin0)) {
+        if (!wait1(&sh.q_full[x], q_ph[x])) return false;
+        q_ph[x] ^= 1;
+      }
+      tc_after();
+      const uint32_t q = smem_u32(sh.q[x]), k = smem_u32(sh.half[hs]);
+#pragma unroll
+      for (int i = 0; i < D / 16; ++i) {
+        const uint32_t o = (i >> 2) * (kTile * 128) + (i & 3) * 32;
+        tc_mma_ss(s_t[x], desc_k(q + o), desc_k(k + o), kIdescS, i > 0);
+      }
+      tc_commit(&sh.s_full[x]);
+      if (flags & (x ? kEnd1 : kEnd0)) tc_commit(&sh.q_free[x]);
+      return true;
+    };
+    auto product_o = [&](int x, int hs, int flags) {
+      if (!wait1(&sh.p_ready[x], p_ph[x])) return false;
+      p_ph[x] ^= 1;
+      if (flags & (x ? kBegin1 : kBegin0)) {
+        if (segs[x]++) {
+          if (!wait1(&sh.o_free[x], of_ph[x])) return false;
+          of_ph[x] ^= 1;
+        }
+      }
+      tc_after();
+      const uint32_t v = smem_u32(sh.half[hs]);
+      const uint32_t more = (flags & (x ? kBegin1 : kBegin0)) ? 0u : 1u;
+#pragma unroll
+      for (int i = 0; i < kTile / 16; ++i)
+        tc_mma_ts(o_t[x], s_t[x] + i * 8, desc_mn(v + i * 2048), kIdescO, i > 0 ? 1u : more);
+      tc_commit(&sh.o_full[x]);
+      return true;
+    };
+    // the flags of the next tile with keys (0: none left)
+    int it = 0;
+    auto take = [&]() -> int {
+      for (;;) {
+        const int mi = it % kMetaSlots;
+        if (!wait1(&sh.meta_full[mi], (it / kMetaSlots) & 1)) return -1;
+        const int f = sh.meta[mi].flags;
+        if (f & kStop) return 0;
+        ++it;
+        mbar_arrive(&sh.meta_empty[mi]);
+        if (f & (kAct0 | kAct1)) return f;
+      }
+    };
+    int cur = take();
+    if (cur > 0) {
+      const int hs = n % kHalfSlots;
+      ok = wait1(&sh.half_full[hs], (n / kHalfSlots) & 1);
+      for (int x = 0; x < 2 && ok; ++x)
+        if (cur & (x ? kAct1 : kAct0)) ok = product_s(x, hs, cur);
+      if (ok) tc_commit(&sh.half_empty[hs]);
+      ++n;
+    }
+    while (ok && cur > 0) {
+      const int next = take();
+      if (next < 0) break;
+      const int vs = n % kHalfSlots, ks = (n + 1) % kHalfSlots;
+      const uint32_t v_ph = (n / kHalfSlots) & 1, k_ph = ((n + 1) / kHalfSlots) & 1;
+      n += 2;
+      if (!(ok = wait1(&sh.half_full[vs], v_ph))) break;
+      // within a segment S0 of the next tile goes between the two O products; at its end both come first
+      const bool same = next > 0 && !(next & kBegin);
+      bool have_k = false;
+      for (int x = 0; x < 2 && ok; ++x) {
+        if (cur & (x ? kAct1 : kAct0)) ok = product_o(x, vs, cur);
+        if (ok && same && (next & (x ? kAct1 : kAct0))) {
+          if (x == 1 && ok) tc_commit(&sh.half_empty[vs]);
+          if (!have_k) ok = wait1(&sh.half_full[ks], k_ph);
+          have_k = true;
+          if (ok) ok = product_s(x, ks, next);
+        } else if (x == 1 && ok) {
+          tc_commit(&sh.half_empty[vs]);
+        }
+      }
+      if (ok && next > 0) {
+        if (!same) {
+          ok = wait1(&sh.half_full[ks], k_ph);
+          for (int x = 0; x < 2 && ok; ++x)
+            if (next & (x ? kAct1 : kAct0)) ok = product_s(x, ks, next);
+        }
+        if (ok) tc_commit(&sh.half_empty[ks]);
+      }
+      cur = next;
+    }
+    // everything issued has finished before tensor memory is given back
+    tc_commit(&sh.done);
+    wait_sleep_teardown(&sh.done, 0);
+  }
+
+  tc_before();
+  __syncthreads();
+  if (warp == 13) {
+    tc_after();
+    asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
+  }
+}
+
+// Joins the parts of the item that starts in CTA blockIdx.x's run, one row
+// per warp, the parts in order.
+template <typename T, int D>
+__global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ AttentionParams p) {
+  constexpr int V = D / 32;
+  pdl_launch();
+  pdl_wait();
+  const Join j = p.joins[blockIdx.x];
+  if (j.last < 0) return;
+  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
+  if (r >= j.rows) return;
+  const int c0 = blockIdx.x, n = j.last - c0 + 1;
+  auto part = [&](int i) { return p.part + int64_t(i == 0 ? j.slot : 2 * (c0 + i)) * (kPairRows * (D + 2)); };
+  float top = -INFINITY;
+  for (int i = 0; i < n; ++i) top = fmaxf(top, part(i)[kPairRows * D + 2 * r]);
+  float sum = 0.0f, o[V];
+#pragma unroll
+  for (int e = 0; e < V; ++e) o[e] = 0.0f;
+#pragma unroll 2
+  for (int i = 0; i < n; ++i) {
+    const float2 st = *reinterpret_cast<const float2*>(part(i) + kPairRows * D + 2 * r);
+    const float f = st.x == -INFINITY ? 0.0f : exp2_fast(st.x - top);
+    sum = fmaf(f, st.y, sum);
+    const float* src = part(i) + r * D + lane * V;
+    if constexpr (V == 4) {
+      const float4 y = *reinterpret_cast<const float4*>(src);
+      o[0] = fmaf(f, y.x, o[0]);
+      o[1] = fmaf(f, y.y, o[1]);
+      o[2] = fmaf(f, y.z, o[2]);
+      o[3] = fmaf(f, y.w, o[3]);
+    } else {
+      const float2 y = *reinterpret_cast<const float2*>(src);
+      o[0] = fmaf(f, y.x, o[0]);
+      o[1] = fmaf(f, y.y, o[1]);
+    }
+  }
+  const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
+  const int row = j.row0 + r;
+  uint16_t* dst = p.out + int64_t(j.t0 + row / p.group) * p.out_stride +
+                  int64_t(j.head * p.group + row % p.group) * D + lane * V;
+  if constexpr (V == 4)
+    *reinterpret_cast<uint2*>(dst) =
+        make_uint2(Half16<T>::pack(o[0] * inv, o[1] * inv), Half16<T>::pack(o[2] * inv, o[3] * inv));
+  else
+    *reinterpret_cast<uint32_t*>(dst) = Half16<T>::pack(o[0] * inv, o[1] * inv);
+}
