@@ -845,7 +845,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), plan.v.threads, plan.v.smem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&lc, plan.v.main, map_k, map_v, p);
   if (e == cudaSuccess && many) {
-    lc = overlapped(dim3(unsigned(plan.grid), kPairRows / 8), 256, 0, stream, &attr);
+    lc = overlapped(dim3(unsigned(plan.grid), kPairRows / 32), 256, 0, stream, &attr);
     e = cudaLaunchKernelEx(&lc, plan.v.join_rows, p);
   } else if (e == cudaSuccess) {
     lc = overlapped(dim3(unsigned(plan.grid), kJoinRows), kJoinThreads, plan.grid * sizeof(float), stream, &attr);

@@ -19,9 +19,11 @@
 //             passes it by more than 8 (log2 units), so the outputs in tensor
 //             memory are almost never rescaled and a tile needs one pass.
 //   8-11      codes to fp16 (exact) in the tensor core's 128-byte-swizzled
-//             layout: keys K-major, values as they lie (MN-major); q rows.
+//             layout: keys K-major, values as they lie (MN-major).
 //   12        pages, scales and the tiles' descriptions, TMA of the codes.
 //   13        the products: S0 = Q0 K^T, S1 = Q1 K^T, O0 += P0 V, O1 += P1 V.
+//   14, 15    q rows to fp16, a segment ahead.
+// Registers move from the last two warpgroups to the softmax's.
 // Tensor memory: S0, S1 (128 columns each; P lies over its S), O0, O1.
 //
 // Work is laid end to end in units of 128 keys and cut evenly over the CTAs,
@@ -29,7 +31,11 @@
 
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
-constexpr int kPreThreads = 14 * 32;
+constexpr int kPreThreads = 16 * 32;
+constexpr int kMoreRegs = 176, kLessRegs = 80;   // 2 * 176 + 2 * 80 = 4 * 128, what the launch holds
+// What a segment costs beyond its tiles (q rows, first S, epilogue), in tiles: the schedule counts every item as
+// that much longer.
+constexpr int kSegmentCost = 2;
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
 enum : int {                                   // PreMeta::flags
@@ -85,19 +91,61 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(accumulate)
       : "memory");
 }
-// this warp's 32 lanes x 32 columns (with the wait in the same statement: nothing may read r before it)
+// One lane of a converged warp. The tensor core's instructions take uniform
+// operands: behind this predicate the compiler issues them as they are,
+// behind `lane == 0` it wraps each one (about 150 cycles instead of 64 for a
+// 128 x 128 x 16 product).
+__device__ __forceinline__ bool elect_one() {
+  uint32_t p;
+  asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
+  return p != 0;
+}
+// this warp's 32 lanes x 32 columns, complete after tc_ld_done on the same registers
 __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
-      "tcgen05.wait::ld.sync.aligned;"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(a)
       : "memory");
+}
+// (the registers are its operands, so that nothing reads them before it)
+__device__ __forceinline__ void tc_ld_done(uint32_t (&r)[32]) {
+  asm volatile("tcgen05.wait::ld.sync.aligned;"
+               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
+                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
+                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
+                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
+                 "+r"(r[30]), "+r"(r[31])
+               :
+               : "memory");
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
+}
+// 32 bytes to a 32-byte-aligned address
+__device__ __forceinline__ void st_global_32(void* p, const uint4& a, const uint4& b) {
+  asm volatile("st.global.v8.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8};" ::"l"(p), "r"(a.x), "r"(a.y), "r"(a.z), "r"(a.w),
+               "r"(b.x), "r"(b.y), "r"(b.z), "r"(b.w)
+               : "memory");
 }
 __device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
   asm volatile(
@@ -167,7 +215,7 @@ __device__ __forceinline__ Pair pair_of(const AttentionParams& p, const Seq& s, 
 __device__ __forceinline__ int64_t pair_units(const AttentionParams& p, const Seq& s, int lane) {
   const int pairs = (s.n * p.group + kPairRows - 1) / kPairRows;
   int64_t sum = 0;
-  for (int i = lane; i < pairs; i += 32) sum += pair_of(p, s, i * kPairRows).tiles;
+  for (int i = lane; i < pairs; i += 32) sum += pair_of(p, s, i * kPairRows).tiles + kSegmentCost;
 #pragma unroll
   for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
   return sum * p.n_kv_heads;
@@ -197,7 +245,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMetaSlots; ++i) {
       mbar_init(&sh.meta_full[i], 33);
-      mbar_init(&sh.meta_empty[i], 13);        // 8 softmax and 4 converting warps, the products' thread
+      mbar_init(&sh.meta_empty[i], 15);        // all warps but the one that writes it
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -208,7 +256,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       mbar_init(&sh.half_empty[i], 1);
     }
     for (int x = 0; x < 2; ++x) {
-      mbar_init(&sh.q_full[x], 4);
+      mbar_init(&sh.q_full[x], 2);
       mbar_init(&sh.q_free[x], 1);
       mbar_init(&sh.s_full[x], 1);
       mbar_init(&sh.p_ready[x], 4);
@@ -237,10 +285,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
 
   if (warp < 8) {
     // -------------------------------------------------------------- softmax
+    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs));
     const int x = warp >> 2, row = threadIdx.x & (kTile - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
     const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 2 * kTile + x * D;
-    float m = -INFINITY, l = 0.0f, factor = 0.0f;
+    float m = -INFINITY, l = 0.0f, factor = p.scale_log2;
     int pv = 0, p_row = 0, p_low = 0, p_high = 0;      // pv: products into O in this segment
     uint32_t s_ph = 0, o_ph = 0;                       // parity of the next S, of the next O
     uint32_t seg = 0;
@@ -260,50 +309,61 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         p_row = me.past + (r0 + row) / p.group;
       }
       if (flags & (x ? kAct1 : kAct0)) {
-        if (!wait(&sh.s_full[x], s_ph)) break;
-        s_ph ^= 1;
-        tc_after();
-        if (pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];   // written before S was computed
         const int pos = me.pos;
         const bool all = pos + kTile - 1 <= p_low &&
                          (p.window == 0 || pos > p_high - p.window || pos + kTile <= p.sinks);
         const int hi = p_row - pos, lo = p.window ? hi - p.window + 1 : 0, sk = p.window ? p.sinks - pos : 0;
+        // lane b: the constants of block b
+        const float ks = me.ks[lane & 7], vs = me.vs[lane & 7];
+        const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
+        if (!wait(&sh.s_full[x], s_ph)) break;
+        s_ph ^= 1;
+        tc_after();
+        // (written before the row tile's first S was computed)
+        if (std::is_same<T, __nv_bfloat16>::value && pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];
         uint32_t pk[kTile / 2];
         float top, sum;
-        // weights of the row against m; top is the largest logit above m
+        // weights of the row against m, and its largest logit
         auto weigh = [&](auto masked, auto weights) {
           const float base = m == -INFINITY ? 0.0f : m;
-          top = -INFINITY;
+          float top0 = -INFINITY, top1 = -INFINITY;
           sum = 0.0f;
+          uint32_t r[2][32];
+          tc_ld32(ts, r[0]);
+          tc_ld_done(r[0]);
 #pragma unroll
           for (int c = 0; c < kTile / 32; ++c) {
-            uint32_t r[32];
-            tc_ld32(ts + c * 32, r);
+            if (c + 1 < kTile / 32) tc_ld32(ts + (c + 1) * 32, r[(c + 1) & 1]);
 #pragma unroll
             for (int h = 0; h < 2; ++h) {
-              const float vs = me.vs[2 * c + h];
-              const float a = factor * me.ks[2 * c + h], b = __log2f(vs) - base, iv = __fdividef(1.0f, vs);
-              float part = 0.0f;
+              const int b = 2 * c + h;
+              const float fa = factor * __shfl_sync(0xffffffffu, ks, b), fb = __shfl_sync(0xffffffffu, lv, b) - base;
+              float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
               for (int e = 0; e < 16; e += 2) {
-                float t[2];
-#pragma unroll
-                for (int f = 0; f < 2; ++f) {
-                  const int j = 32 * c + 16 * h + e + f;
-                  t[f] = fmaf(__uint_as_float(r[16 * h + e + f]), a, b);
-                  if (decltype(masked)::value && !(j <= hi && (j >= lo || j < sk))) t[f] = -INFINITY;
-                  top = fmaxf(top, t[f]);
+                const uint32_t* src = &r[c & 1][16 * h + e];
+                float2 t = fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), make_float2(fa, fa),
+                                make_float2(fb, fb));
+                if (decltype(masked)::value) {
+                  const int k = 16 * b + e;
+                  if (!((k <= hi) & ((k >= lo) | (k < sk)))) t.x = -INFINITY;
+                  if (!((k + 1 <= hi) & ((k + 1 >= lo) | (k + 1 < sk)))) t.y = -INFINITY;
                 }
+                if (h)
+                  top1 = fmaxf(top1, fmaxf(t.x, t.y));
+                else
+                  top0 = fmaxf(top0, fmaxf(t.x, t.y));
                 if (decltype(weights)::value) {
-                  const float w0 = exp2_fast(t[0]), w1 = exp2_fast(t[1]);
-                  part += w0 + w1;
-                  pk[16 * c + 8 * h + e / 2] = Half16<__half>::pack(w0, w1);
+                  const float2 w = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+                  part = add2(part, w);
+                  pk[8 * b + e / 2] = Half16<__half>::pack(w.x, w.y);
                 }
               }
-              if (decltype(weights)::value) sum = fmaf(part, iv, sum);
+              if (decltype(weights)::value) sum = fmaf(part.x + part.y, __shfl_sync(0xffffffffu, iv, b), sum);
             }
+            if (c + 1 < kTile / 32) tc_ld_done(r[(c + 1) & 1]);
           }
-          top += base;
+          top = fmaxf(top0, top1) + base;
         };
         auto pass = [&](auto weights) {
           if (all)
@@ -329,6 +389,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             for (int c = 0; c < D / 32; ++c) {
               uint32_t r[32];
               tc_ld32(to + c * 32, r);
+              tc_ld_done(r);
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
               tc_st32(to + c * 32, r);
@@ -354,6 +415,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         const int gr = me.row0 + r0, dest = me.dest;
         uint16_t* dst = p.out + int64_t(me.t0 + gr / p.group) * p.out_stride +
                         int64_t(me.head * p.group + gr % p.group) * D;
+        const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
         float* part = p.part + int64_t(dest) * (kPairRows * (D + 2));
         if (pv > 0) {
           if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
@@ -365,22 +427,34 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           uint32_t r[32];
           if (pv > 0) {
             tc_ld32(to + c * 32, r);
+            tc_ld_done(r);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0;
           }
           if (mine && dest < 0) {
 #pragma unroll
-            for (int e = 0; e < 32; e += 8) {
-              float v[8];
+            for (int e = 0; e < 32; e += 16) {
+              float v[8], w[8];
 #pragma unroll
-              for (int f = 0; f < 8; ++f) v[f] = __uint_as_float(r[e + f]) * inv;
-              *reinterpret_cast<uint4*>(dst + c * 32 + e) = pack8<T>(v);
+              for (int f = 0; f < 8; ++f) {
+                v[f] = __uint_as_float(r[e + f]) * inv;
+                w[f] = __uint_as_float(r[e + 8 + f]) * inv;
+              }
+              const uint4 a = pack8<T>(v), b = pack8<T>(w);
+              if (wide) {
+                st_global_32(dst + c * 32 + e, a, b);
+              } else {
+                *reinterpret_cast<uint4*>(dst + c * 32 + e) = a;
+                *reinterpret_cast<uint4*>(dst + c * 32 + e + 8) = b;
+              }
             }
           } else if (mine) {
+            // four channels of a row together, rows side by side: the lanes' stores are contiguous
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + r0 * D + c * 32 + e) = make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
+              *reinterpret_cast<uint4*>(part + ((c * 8 + e / 4) * kPairRows + r0) * 4) =
+                  make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
           }
         }
         if (mine && dest >= 0) *reinterpret_cast<float2*>(part + kPairRows * D + 2 * r0) = make_float2(m, l);
@@ -395,10 +469,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
     }
   } else if (warp < 12) {
-    // ----------------------------------------------- codes and q rows to fp16
+    // ---------------------------------------------------------- codes to fp16
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     const int tid = threadIdx.x - 8 * 32;
-    uint32_t q_ph[2] = {0, 0}, seg = 0;
-    int used[2] = {0, 0};
     int n = 0;                                  // tiles of codes converted
     for (int it = 0;; ++it) {
       const int mi = it % kMetaSlots;
@@ -406,64 +479,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const PreMeta& me = sh.meta[mi];
       const int flags = me.flags, valid = me.valid;
       if (flags & kStop) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+      if (!(flags & (kAct0 | kAct1))) continue;  // a tile without keys
       bool ok = true;
-      if (flags & kBegin) {
-        for (int x = 0; x < 2 && ok; ++x) {
-          if (!(flags & (x ? kHas1 : kHas0))) continue;
-          // the row from memory while the buffer's last products finish
-          const int r = x * kTile + tid, gr = me.row0 + r;
-          uint4 v[D / 8];
-          const uint16_t* src = p.q + int64_t(me.t0 + gr / p.group) * p.q_stride +
-                                int64_t(me.head * p.group + gr % p.group) * D;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            v[i] = r < me.rows ? reinterpret_cast<const uint4*>(src)[i] : make_uint4(0, 0, 0, 0);
-          float f = 1.0f;
-          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
-            float top = 0.0f;
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              float y[8];
-              unpack8<T>(v[i], y);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
-            }
-            const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
-            f = __uint_as_float(e << 23);
-            const float inv = __uint_as_float((254u - e) << 23);
-#pragma unroll
-            for (int i = 0; i < D / 8; ++i) {
-              float y[8];
-              unpack8<T>(v[i], y);
-#pragma unroll
-              for (int j = 0; j < 8; ++j) y[j] *= inv;
-              v[i] = pack8<__half>(y);
-            }
-          }
-          if (used[x]++) {
-            if (!wait(&sh.q_free[x], q_ph[x])) {
-              ok = false;
-              break;
-            }
-            q_ph[x] ^= 1;
-          }
-          uint8_t* dst = sh.q[x] + tid * 128;
-#pragma unroll
-          for (int i = 0; i < D / 8; ++i)
-            *reinterpret_cast<uint4*>(dst + (i >> 3) * (kTile * 128) + (((i & 7) ^ (tid & 7)) << 4)) = v[i];
-          sh.factor[seg % kMetaSlots][x][tid] = f;
-          fence_proxy_async_smem();
-          __syncwarp();
-          if (lane == 0) mbar_arrive(&sh.q_full[x]);
-        }
-      }
-      if (flags & kEnd) ++seg;
-      if (!ok) break;
-      if (!(flags & (kAct0 | kAct1))) {         // a tile without keys
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
-        continue;
-      }
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const int rs = n % kRawSlots, hs = n % kHalfSlots;
         if (!wait(&sh.raw_full[rs], (n / kRawSlots) & 1) || !wait(&sh.half_empty[hs], ((n / kHalfSlots) & 1) ^ 1)) {
@@ -497,11 +516,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         }
       }
       if (!ok) break;
-      __syncwarp();
-      if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
     }
   } else if (warp == 12) {
     // --------------------------------------------- the schedule, pages, copies
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     int64_t total = 0;
     const Batch& a = p.batch;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
@@ -537,7 +555,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         u += units;
         int start = 0;                           // the pair that holds unit u0, 32 looked at together
         while (start < pairs) {
-          int inc = start + lane < pairs ? pair_of(p, s, (start + lane) * kPairRows).tiles : 0;
+          int inc = start + lane < pairs ? pair_of(p, s, (start + lane) * kPairRows).tiles + kSegmentCost : 0;
           const int own = inc;
 #pragma unroll
           for (int o = 1; o < 32; o <<= 1) {
@@ -556,14 +574,16 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         }
         for (int pr = start; pr < pairs && begin < u1 && ok; ++pr) {
           const Pair pa = pair_of(p, s, pr * kPairRows);
-          const int64_t width = int64_t(pa.tiles) * p.n_kv_heads;
-          int head = u0 > begin ? int((u0 - begin) / pa.tiles) : 0;
-          for (; head < p.n_kv_heads && begin + int64_t(head) * pa.tiles < u1 && ok; ++head) {
-            const int64_t first = begin + int64_t(head) * pa.tiles, end = first + pa.tiles;
+          const int span = pa.tiles + kSegmentCost;      // the item's units: its cost, then its tiles
+          const int64_t width = int64_t(span) * p.n_kv_heads;
+          int head = u0 > begin ? int((u0 - begin) / span) : 0;
+          for (; head < p.n_kv_heads && begin + int64_t(head) * span < u1 && ok; ++head) {
+            const int64_t first = begin + int64_t(head) * span + kSegmentCost, end = first + pa.tiles;
             const int v0 = int(max(u0 - first, int64_t(0))), v1 = int(min(u1 - first, int64_t(pa.tiles)));
-            const bool whole = first >= u0 && end <= u1;
-            const int dest = whole ? -1 : int(2 * blockIdx.x) + (first > u0);
-            if (first >= u0 && end > u1) {
+            if (v1 <= v0) continue;
+            // a part that starts its item goes to the CTA's second place, one that continues it to the first
+            const int dest = v0 == 0 && v1 == pa.tiles ? -1 : int(2 * blockIdx.x) + (v0 == 0);
+            if (v0 == 0 && v1 < pa.tiles) {
               join.last = int((end - 1) / per);
               join.slot = dest;
               join.t0 = s.t0;
@@ -587,8 +607,16 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
               lo[x] = __reduce_min_sync(0xffffffffu, lo[x]);
               hi[x] = __reduce_max_sync(0xffffffffu, hi[x]);
             }
+            // lane i: block i of the keys, lane 8 + i: of the values; a tile's page ids load while the one before
+            // it is handed out
+            auto id_of = [&](int v) {
+              const int blk = tile_of(v) * kTile + (lane & 7) * kBlock;
+              return v < v1 && lane < 16 && blk < s.len ? table[blk / a.page_size] : -1;
+            };
+            int id = id_of(v0);
             for (int v = v0; v < v1; ++v, ++it) {
               const int mi = it % kMetaSlots, pos = tile_of(v) * kTile;
+              const int id_next = id_of(v + 1);
               int flags = (v == v0 ? kBegin : 0) | (v == v1 - 1 ? kEnd : 0);
               for (int x = 0; x < 2; ++x) {
                 if (hi[x] >= 0) flags |= x ? kHas1 : kHas0;
@@ -597,10 +625,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
                 if (v == hi[x]) flags |= x ? kEnd1 : kEnd0;
               }
               const bool keys = flags & (kAct0 | kAct1);
-              // lane i: block i of the keys, lane 8 + i: of the values
               const int blk = pos + (lane & 7) * kBlock;
               int page = -1;
-              if (keys && lane < 16 && blk < s.len) page = checked_page(a, table[blk / a.page_size], err);
+              if (keys && lane < 16 && blk < s.len) page = checked_page(a, id, err);
+              id = id_next;
               const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
               if (!wait(&sh.meta_empty[mi], ((it / kMetaSlots) & 1) ^ 1)) {
                 ok = false;
@@ -668,49 +696,60 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // every copy issued has landed before the CTA's shared memory goes
     for (int i = max(0, n - kRawSlots); i < n; ++i)
       wait_sleep_teardown(&sh.raw_full[i % kRawSlots], (i / kRawSlots) & 1);
-  } else if (lane == 0) {
+  } else if (warp == 13) {
     // ----------------------------------------------------------- the products
     // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
     // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
-    auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_sleep(bar, parity, abort, err, kErrWait); };
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, of_ph[2] = {0, 0};
     int segs[2] = {0, 0};                        // segments the row tile's O was used in
     int n = 0;                                   // code tiles taken
-    const uint32_t s_t[2] = {tmem, tmem + kTile}, o_t[2] = {tmem + 2 * kTile, tmem + 2 * kTile + D};
     bool ok = true;
+    auto commit = [&](uint64_t* bar) {
+      if (elect_one()) tc_commit(bar);
+      __syncwarp();
+    };
     // S = Q K^T of row tile x
     auto product_s = [&](int x, int hs, int flags) {
       if (flags & (x ? kBegin1 : kBegin0)) {
-        if (!wait1(&sh.q_full[x], q_ph[x])) return false;
+        if (!wait(&sh.q_full[x], q_ph[x])) return false;
         q_ph[x] ^= 1;
       }
       tc_after();
-      const uint32_t q = smem_u32(sh.q[x]), k = smem_u32(sh.half[hs]);
+      const uint64_t q = desc_k(smem_u32(sh.q[x])), k = desc_k(smem_u32(sh.half[hs]));
+      const uint32_t d = tmem + x * kTile;
+      if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < D / 16; ++i) {
-        const uint32_t o = (i >> 2) * (kTile * 128) + (i & 3) * 32;
-        tc_mma_ss(s_t[x], desc_k(q + o), desc_k(k + o), kIdescS, i > 0);
+        for (int i = 0; i < D / 16; ++i) {
+          constexpr int kStep = 32 >> 4;         // 16 channels, in the descriptor's units
+          const int o = (i >> 2) * (kTile * 128 >> 4) + (i & 3) * kStep;
+          tc_mma_ss(d, q + o, k + o, kIdescS, i > 0);
+        }
+        tc_commit(&sh.s_full[x]);
+        if (flags & (x ? kEnd1 : kEnd0)) tc_commit(&sh.q_free[x]);
       }
-      tc_commit(&sh.s_full[x]);
-      if (flags & (x ? kEnd1 : kEnd0)) tc_commit(&sh.q_free[x]);
+      __syncwarp();
       return true;
     };
     auto product_o = [&](int x, int hs, int flags) {
-      if (!wait1(&sh.p_ready[x], p_ph[x])) return false;
+      if (!wait(&sh.p_ready[x], p_ph[x])) return false;
       p_ph[x] ^= 1;
       if (flags & (x ? kBegin1 : kBegin0)) {
         if (segs[x]++) {
-          if (!wait1(&sh.o_free[x], of_ph[x])) return false;
+          if (!wait(&sh.o_free[x], of_ph[x])) return false;
           of_ph[x] ^= 1;
         }
       }
       tc_after();
-      const uint32_t v = smem_u32(sh.half[hs]);
+      const uint64_t v = desc_mn(smem_u32(sh.half[hs]));
       const uint32_t more = (flags & (x ? kBegin1 : kBegin0)) ? 0u : 1u;
+      const uint32_t d = tmem + 2 * kTile + x * D, w = tmem + x * kTile;
+      if (elect_one()) {
 #pragma unroll
-      for (int i = 0; i < kTile / 16; ++i)
-        tc_mma_ts(o_t[x], s_t[x] + i * 8, desc_mn(v + i * 2048), kIdescO, i > 0 ? 1u : more);
-      tc_commit(&sh.o_full[x]);
+        for (int i = 0; i < kTile / 16; ++i) tc_mma_ts(d, w + i * 8, v + i * (2048 >> 4), kIdescO, i > 0 ? 1u : more);
+        tc_commit(&sh.o_full[x]);
+      }
+      __syncwarp();
       return true;
     };
     // the flags of the next tile with keys (0: none left)
@@ -718,21 +757,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     auto take = [&]() -> int {
       for (;;) {
         const int mi = it % kMetaSlots;
-        if (!wait1(&sh.meta_full[mi], (it / kMetaSlots) & 1)) return -1;
+        if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) return -1;
         const int f = sh.meta[mi].flags;
         if (f & kStop) return 0;
         ++it;
-        mbar_arrive(&sh.meta_empty[mi]);
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
         if (f & (kAct0 | kAct1)) return f;
       }
     };
     int cur = take();
     if (cur > 0) {
       const int hs = n % kHalfSlots;
-      ok = wait1(&sh.half_full[hs], (n / kHalfSlots) & 1);
+      ok = wait(&sh.half_full[hs], (n / kHalfSlots) & 1);
       for (int x = 0; x < 2 && ok; ++x)
         if (cur & (x ? kAct1 : kAct0)) ok = product_s(x, hs, cur);
-      if (ok) tc_commit(&sh.half_empty[hs]);
+      if (ok) commit(&sh.half_empty[hs]);
       ++n;
     }
     while (ok && cur > 0) {
@@ -741,34 +781,111 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const int vs = n % kHalfSlots, ks = (n + 1) % kHalfSlots;
       const uint32_t v_ph = (n / kHalfSlots) & 1, k_ph = ((n + 1) / kHalfSlots) & 1;
       n += 2;
-      if (!(ok = wait1(&sh.half_full[vs], v_ph))) break;
+      if (!(ok = wait(&sh.half_full[vs], v_ph))) break;
       // within a segment S0 of the next tile goes between the two O products; at its end both come first
       const bool same = next > 0 && !(next & kBegin);
       bool have_k = false;
       for (int x = 0; x < 2 && ok; ++x) {
         if (cur & (x ? kAct1 : kAct0)) ok = product_o(x, vs, cur);
+        if (ok && x == 1) commit(&sh.half_empty[vs]);
         if (ok && same && (next & (x ? kAct1 : kAct0))) {
-          if (x == 1 && ok) tc_commit(&sh.half_empty[vs]);
-          if (!have_k) ok = wait1(&sh.half_full[ks], k_ph);
+          if (!have_k) ok = wait(&sh.half_full[ks], k_ph);
           have_k = true;
           if (ok) ok = product_s(x, ks, next);
-        } else if (x == 1 && ok) {
-          tc_commit(&sh.half_empty[vs]);
         }
       }
       if (ok && next > 0) {
         if (!same) {
-          ok = wait1(&sh.half_full[ks], k_ph);
+          ok = wait(&sh.half_full[ks], k_ph);
           for (int x = 0; x < 2 && ok; ++x)
             if (next & (x ? kAct1 : kAct0)) ok = product_s(x, ks, next);
         }
-        if (ok) tc_commit(&sh.half_empty[ks]);
+        if (ok) commit(&sh.half_empty[ks]);
       }
       cur = next;
     }
     // everything issued has finished before tensor memory is given back
-    tc_commit(&sh.done);
+    commit(&sh.done);
     wait_sleep_teardown(&sh.done, 0);
+  } else {
+    // ------------------------------------------------------------------ q rows
+    // Each warp brings 64 rows of both tiles: asynchronous copies into their swizzled places, then, for bf16, a
+    // turn in place to fp16 over a power of two of the row's largest magnitude.
+    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
+    constexpr int CPR = D / 8;                   // 16-byte chunks of a row
+    const int r_first = (warp - 14) * 64;
+    uint32_t q_ph[2] = {0, 0}, seg = 0;
+    int used[2] = {0, 0};
+    for (int it = 0;; ++it) {
+      const int mi = it % kMetaSlots;
+      if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) break;
+      const PreMeta& me = sh.meta[mi];
+      const int flags = me.flags, t0 = me.t0, row0 = me.row0, rows = me.rows, head = me.head;
+      if (flags & kStop) break;
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+      bool ok = true;
+      if (flags & kBegin) {
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(flags & (x ? kHas1 : kHas0))) continue;
+          if (used[x]++) {
+            ok = wait(&sh.q_free[x], q_ph[x]);
+            q_ph[x] ^= 1;
+            if (!ok) break;
+          }
+          const uint32_t dst = smem_u32(sh.q[x]);
+          for (int i = lane; i < 64 * CPR; i += 32) {
+            const int r = r_first + i / CPR, c = i % CPR, gr = row0 + x * kTile + r;
+            const bool there = x * kTile + r < rows;
+            const uint16_t* src = p.q;
+            if (there)
+              src += int64_t(t0 + gr / p.group) * p.q_stride + int64_t(head * p.group + gr % p.group) * D + c * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
+                             dst + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
+                         "l"(src), "r"(there ? 16 : 0)
+                         : "memory");
+          }
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+        __syncwarp();
+        for (int x = 0; x < 2 && ok; ++x) {
+          if (!(flags & (x ? kHas1 : kHas0))) continue;
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) {
+#pragma unroll 1
+            for (int r = r_first + lane; r < r_first + 64; r += 32) {
+              uint8_t* src = sh.q[x] + r * 128;
+              auto chunk = [&](int c) {
+                return reinterpret_cast<uint4*>(src + (c >> 3) * (kTile * 128) + (((c & 7) ^ (r & 7)) << 4));
+              };
+              float top = 0.0f;
+#pragma unroll 4
+              for (int c = 0; c < CPR; ++c) {
+                float y[8];
+                unpack8<T>(*chunk(c), y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(y[j]));
+              }
+              const uint32_t e = min(max(__float_as_uint(top) >> 23, 1u), 253u);
+              const float inv = __uint_as_float((254u - e) << 23);
+              sh.factor[seg % kMetaSlots][x][r] = __uint_as_float(e << 23);
+#pragma unroll 4
+              for (int c = 0; c < CPR; ++c) {
+                float y[8];
+                unpack8<T>(*chunk(c), y);
+#pragma unroll
+                for (int j = 0; j < 8; ++j) y[j] *= inv;
+                *chunk(c) = pack8<__half>(y);
+              }
+            }
+          }
+          fence_proxy_async_smem();
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.q_full[x]);
+        }
+      }
+      if (flags & kEnd) ++seg;
+      if (!ok) break;
+    }
   }
 
   tc_before();
@@ -779,49 +896,52 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   }
 }
 
-// Joins the parts of the item that starts in CTA blockIdx.x's run, one row
-// per warp, the parts in order.
+// Joins the parts of the item that starts in CTA blockIdx.x's run, 32 rows to
+// a block: lane = row, a warp the channels 4 w .. of each 32; parts in order.
 template <typename T, int D>
 __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ AttentionParams p) {
-  constexpr int V = D / 32;
+  constexpr int kRow = D * 2 + 16;
+  __shared__ __align__(16) uint8_t tile[32 * kRow];
   pdl_launch();
   pdl_wait();
   const Join j = p.joins[blockIdx.x];
-  if (j.last < 0) return;
-  const int r = blockIdx.y * 8 + (threadIdx.x >> 5), lane = threadIdx.x & 31;
-  if (r >= j.rows) return;
+  if (j.last < 0 || int(blockIdx.y) * 32 >= j.rows) return;
+  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  const int r = blockIdx.y * 32 + lane;          // (rows behind the item's read what is there and are not written)
   const int c0 = blockIdx.x, n = j.last - c0 + 1;
   auto part = [&](int i) { return p.part + int64_t(i == 0 ? j.slot : 2 * (c0 + i)) * (kPairRows * (D + 2)); };
-  float top = -INFINITY;
-  for (int i = 0; i < n; ++i) top = fmaxf(top, part(i)[kPairRows * D + 2 * r]);
-  float sum = 0.0f, o[V];
+  float top = -INFINITY, sum = 0.0f;
+  const bool mine = r < j.rows;
+  for (int i = 0; i < n && mine; ++i) top = fmaxf(top, part(i)[kPairRows * D + 2 * r]);
+  float4 o[D / 32];
 #pragma unroll
-  for (int e = 0; e < V; ++e) o[e] = 0.0f;
+  for (int e = 0; e < D / 32; ++e) o[e] = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 2
-  for (int i = 0; i < n; ++i) {
+  for (int i = 0; i < n && mine; ++i) {
     const float2 st = *reinterpret_cast<const float2*>(part(i) + kPairRows * D + 2 * r);
     const float f = st.x == -INFINITY ? 0.0f : exp2_fast(st.x - top);
     sum = fmaf(f, st.y, sum);
-    const float* src = part(i) + r * D + lane * V;
-    if constexpr (V == 4) {
-      const float4 y = *reinterpret_cast<const float4*>(src);
-      o[0] = fmaf(f, y.x, o[0]);
-      o[1] = fmaf(f, y.y, o[1]);
-      o[2] = fmaf(f, y.z, o[2]);
-      o[3] = fmaf(f, y.w, o[3]);
-    } else {
-      const float2 y = *reinterpret_cast<const float2*>(src);
-      o[0] = fmaf(f, y.x, o[0]);
-      o[1] = fmaf(f, y.y, o[1]);
+#pragma unroll
+    for (int e = 0; e < D / 32; ++e) {
+      const float4 y = *reinterpret_cast<const float4*>(part(i) + ((e * 8 + warp) * kPairRows + r) * 4);
+      o[e].x = fmaf(f, y.x, o[e].x);
+      o[e].y = fmaf(f, y.y, o[e].y);
+      o[e].z = fmaf(f, y.z, o[e].z);
+      o[e].w = fmaf(f, y.w, o[e].w);
     }
   }
   const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
-  const int row = j.row0 + r;
-  uint16_t* dst = p.out + int64_t(j.t0 + row / p.group) * p.out_stride +
-                  int64_t(j.head * p.group + row % p.group) * D + lane * V;
-  if constexpr (V == 4)
-    *reinterpret_cast<uint2*>(dst) =
-        make_uint2(Half16<T>::pack(o[0] * inv, o[1] * inv), Half16<T>::pack(o[2] * inv, o[3] * inv));
-  else
-    *reinterpret_cast<uint32_t*>(dst) = Half16<T>::pack(o[0] * inv, o[1] * inv);
+#pragma unroll
+  for (int e = 0; e < D / 32; ++e)
+    *reinterpret_cast<uint2*>(tile + lane * kRow + (e * 8 + warp) * 8) =
+        make_uint2(Half16<T>::pack(o[e].x * inv, o[e].y * inv), Half16<T>::pack(o[e].z * inv, o[e].w * inv));
+  __syncthreads();
+  constexpr int CPR = D / 8;
+  for (int i = threadIdx.x; i < 32 * CPR; i += 256) {
+    const int q = i / CPR, c = i % CPR, row = j.row0 + blockIdx.y * 32 + q;
+    if (int(blockIdx.y) * 32 + q >= j.rows) break;
+    *reinterpret_cast<uint4*>(p.out + int64_t(j.t0 + row / p.group) * p.out_stride +
+                              int64_t(j.head * p.group + row % p.group) * D + c * 8) =
+        *reinterpret_cast<const uint4*>(tile + q * kRow + c * 16);
+  }
 }
