@@ -32,10 +32,11 @@
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
 constexpr int kPreThreads = 16 * 32;
-constexpr int kMoreRegs = 176, kLessRegs = 80;   // 2 * 176 + 2 * 80 = 4 * 128, what the launch holds
+constexpr int kMoreRegs = 144, kLessRegs = 112;   // 2 * 144 + 2 * 112 = 4 * 128, what the launch holds
 // What a segment costs beyond its tiles (q rows, first S, epilogue), in tiles: the schedule counts every item as
 // that much longer.
 constexpr int kSegmentCost = 2;
+constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
 enum : int {                                   // PreMeta::flags
@@ -158,6 +159,14 @@ __device__ __forceinline__ void tc_st32(uint32_t a, const uint32_t* r) {
       "r"(r[28]), "r"(r[29]), "r"(r[30]), "r"(r[31])
       : "memory");
 }
+__device__ __forceinline__ void tc_st16(uint32_t a, const uint32_t* r) {
+  asm volatile(
+      "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], "
+      "{%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(a),
+      "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]),
+      "r"(r[10]), "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+      : "memory");
+}
 __device__ __forceinline__ void tc_wait_st() { asm volatile("tcgen05.wait::st.sync.aligned;" ::: "memory"); }
 
 // Shared-memory operand descriptors, 128-byte swizzle. K-major: 8-row groups
@@ -228,13 +237,43 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
   b = make_uint4(code_pair<FMT, 0>(c.z), code_pair<FMT, 2>(c.z), code_pair<FMT, 0>(c.w), code_pair<FMT, 2>(c.w));
 }
 
+// Column k of 32 is visible if k <= hi and (k >= lo or k < sk); the others get `value`.
+__device__ __forceinline__ void mask32(uint32_t (&r)[32], int hi, int lo, int sk, float value) {
+#pragma unroll
+  for (int k = 0; k < 32; ++k)
+    if (!((k <= hi) & ((k >= lo) | (k < sk)))) r[k] = __float_as_uint(value);
+}
+
+template <class Op>
+__device__ __forceinline__ float largest16(const uint32_t* r, Op op) {
+  float a = op(__uint_as_float(r[0]), __uint_as_float(r[1])), b = op(__uint_as_float(r[2]), __uint_as_float(r[3]));
+#pragma unroll
+  for (int e = 4; e < 16; e += 4) {
+    a = op(a, op(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
+    b = op(b, op(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])));
+  }
+  return op(a, b);
+}
+
+// A bounded wait in few instructions (it is inlined in many places).
+__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  for (long long t0 = 0;;) {
+    if (mbar_try_wait_sleep(bar, parity)) return true;
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitCycles || *abort) {
+      *abort = 1;
+      atomicOr(err, kErrWait);
+      return false;
+    }
+  }
+}
+
 template <typename T, int D, int FMT>
 __global__ void __launch_bounds__(kPreThreads, 1)
 prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                          const __grid_constant__ AttentionParams p) {
   using Sh = PreShared<D>;
-  constexpr int kPanels = D / 64;
-  constexpr int kRawBytes = kTile * D;
   constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kTile >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
   extern __shared__ uint8_t smem_raw[];
@@ -280,7 +319,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   const uint32_t tmem = sh.tmem;
   // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_sleep(bar, parity, abort, err, kErrWait)) != 0;
+    return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
   };
 
   if (warp < 8) {
@@ -321,64 +360,28 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         tc_after();
         // (written before the row tile's first S was computed)
         if (std::is_same<T, __nv_bfloat16>::value && pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];
-        uint32_t pk[kTile / 2];
-        float top, sum;
-        // weights of the row against m, and its largest logit
-        auto weigh = [&](auto masked, auto weights) {
-          const float base = m == -INFINITY ? 0.0f : m;
-          float top0 = -INFINITY, top1 = -INFINITY;
-          sum = 0.0f;
-          uint32_t r[2][32];
-          tc_ld32(ts, r[0]);
-          tc_ld_done(r[0]);
-#pragma unroll
-          for (int c = 0; c < kTile / 32; ++c) {
-            if (c + 1 < kTile / 32) tc_ld32(ts + (c + 1) * 32, r[(c + 1) & 1]);
-#pragma unroll
-            for (int h = 0; h < 2; ++h) {
-              const int b = 2 * c + h;
-              const float fa = factor * __shfl_sync(0xffffffffu, ks, b), fb = __shfl_sync(0xffffffffu, lv, b) - base;
-              float2 part = make_float2(0.0f, 0.0f);
-#pragma unroll
-              for (int e = 0; e < 16; e += 2) {
-                const uint32_t* src = &r[c & 1][16 * h + e];
-                float2 t = fma2(make_float2(__uint_as_float(src[0]), __uint_as_float(src[1])), make_float2(fa, fa),
-                                make_float2(fb, fb));
-                if (decltype(masked)::value) {
-                  const int k = 16 * b + e;
-                  if (!((k <= hi) & ((k >= lo) | (k < sk)))) t.x = -INFINITY;
-                  if (!((k + 1 <= hi) & ((k + 1 >= lo) | (k + 1 < sk)))) t.y = -INFINITY;
-                }
-                if (h)
-                  top1 = fmaxf(top1, fmaxf(t.x, t.y));
-                else
-                  top0 = fmaxf(top0, fmaxf(t.x, t.y));
-                if (decltype(weights)::value) {
-                  const float2 w = make_float2(exp2_fast(t.x), exp2_fast(t.y));
-                  part = add2(part, w);
-                  pk[8 * b + e / 2] = Half16<__half>::pack(w.x, w.y);
-                }
-              }
-              if (decltype(weights)::value) sum = fmaf(part.x + part.y, __shfl_sync(0xffffffffu, iv, b), sum);
-            }
-            if (c + 1 < kTile / 32) tc_ld_done(r[(c + 1) & 1]);
+        // Two passes over S, each a rolled loop of 32 columns (straight code for a whole tile misses the
+        // instruction cache). First the row's largest logit.
+        float top = -INFINITY;
+#pragma unroll 1
+        for (int c = 0; c < kTile / 32; ++c) {
+          uint32_t r[32];
+          tc_ld32(ts + c * 32, r);
+          const float a0 = factor * __shfl_sync(0xffffffffu, ks, 2 * c), a1 = factor * __shfl_sync(0xffffffffu, ks, 2 * c + 1);
+          const float b0 = __shfl_sync(0xffffffffu, lv, 2 * c), b1 = __shfl_sync(0xffffffffu, lv, 2 * c + 1);
+          tc_ld_done(r);
+          if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, p.scale_log2 < 0.0f ? INFINITY : -INFINITY);
+          float t0, t1;
+          if (p.scale_log2 >= 0.0f) {
+            t0 = largest16(r, [](float u, float v) { return fmaxf(u, v); });
+            t1 = largest16(r + 16, [](float u, float v) { return fmaxf(u, v); });
+          } else {
+            t0 = largest16(r, [](float u, float v) { return fminf(u, v); });
+            t1 = largest16(r + 16, [](float u, float v) { return fminf(u, v); });
           }
-          top = fmaxf(top0, top1) + base;
-        };
-        auto pass = [&](auto weights) {
-          if (all)
-            weigh(std::false_type{}, weights);
-          else
-            weigh(std::true_type{}, weights);
-        };
-        bool again = true;
-        if (pv > 0) {
-          pass(std::true_type{});
-          again = __any_sync(0xffffffffu, top > m + kSlack);
-        } else {
-          pass(std::false_type{});
+          top = fmaxf(top, fmaxf(fmaf(t0, a0, b0), fmaf(t1, a1, b1)));
         }
-        if (again) {
+        if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float raised = fmaxf(m, top);
           const float f = raised == -INFINITY ? 1.0f : exp2_fast(m - raised);
           if (pv > 0) {
@@ -397,11 +400,43 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           }
           l *= f;
           m = raised;
-          pass(std::true_type{});
         }
-        l += sum;
-        tc_st32(ts, pk);
-        tc_st32(ts + 32, pk + 32);
+        // Then the weights, which take the place of S columns already read.
+        const float base = m == -INFINITY ? 0.0f : m;
+#pragma unroll 1
+        for (int c = 0; c < kTile / 32; ++c) {
+          uint32_t r[32], pk[16];
+          tc_ld32(ts + c * 32, r);
+          float2 fa[2], fb[2], part[2];
+          float is[2];
+#pragma unroll
+          for (int h = 0; h < 2; ++h) {
+            const float a = factor * __shfl_sync(0xffffffffu, ks, 2 * c + h);
+            const float b = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
+            is[h] = __shfl_sync(0xffffffffu, iv, 2 * c + h);
+            fa[h] = make_float2(a, a);
+            fb[h] = make_float2(b, b);
+            part[h] = make_float2(0.0f, 0.0f);
+          }
+          tc_ld_done(r);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const int h = e >> 4;
+            float2 t = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), fa[h], fb[h]);
+            r[e] = __float_as_uint(t.x);
+            r[e + 1] = __float_as_uint(t.y);
+          }
+          if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, -INFINITY);
+#pragma unroll
+          for (int e = 0; e < 32; e += 2) {
+            const float2 w = make_float2(exp2_fast(__uint_as_float(r[e])), exp2_fast(__uint_as_float(r[e + 1])));
+            part[e >> 4] = add2(part[e >> 4], w);
+            pk[e / 2] = Half16<__half>::pack(w.x, w.y);
+          }
+          l = fmaf(part[0].x + part[0].y, is[0], l);
+          l = fmaf(part[1].x + part[1].y, is[1], l);
+          tc_st16(ts + c * 16, pk);
+        }
         tc_wait_st();
         tc_before();
         __syncwarp();
@@ -834,12 +869,19 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             if (!ok) break;
           }
           const uint32_t dst = smem_u32(sh.q[x]);
+          // lane i: where rows i and 32 + i of this warp's lie
+          int64_t at[2];
+#pragma unroll
+          for (int k = 0; k < 2; ++k) {
+            const int gr = row0 + x * kTile + r_first + 32 * k + lane, tok = gr / p.group;
+            at[k] = int64_t(t0 + tok) * p.q_stride + int64_t(head * p.group + gr - tok * p.group) * D;
+          }
+#pragma unroll 4
           for (int i = lane; i < 64 * CPR; i += 32) {
-            const int r = r_first + i / CPR, c = i % CPR, gr = row0 + x * kTile + r;
+            const int k = i / CPR, r = r_first + k, c = i % CPR;
+            const int64_t off = __shfl_sync(0xffffffffu, i < 32 * CPR ? at[0] : at[1], k & 31);
             const bool there = x * kTile + r < rows;
-            const uint16_t* src = p.q;
-            if (there)
-              src += int64_t(t0 + gr / p.group) * p.q_stride + int64_t(head * p.group + gr % p.group) * D + c * 8;
+            const uint16_t* src = there ? p.q + off + c * 8 : p.q;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(
                              dst + (c >> 3) * (kTile * 128) + r * 128 + (((c & 7) ^ (r & 7)) << 4)),
                          "l"(src), "r"(there ? 16 : 0)
