@@ -201,7 +201,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   constexpr int R = 8 * NT;
   using Sh = Shared<D, R>;
   extern __shared__ uint8_t smem_raw[];
-  Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset from the array, not a rounded address: the compiler then knows it is shared memory)
+  Sh& sh = *reinterpret_cast<Sh*>(smem_raw + ((0u - smem_u32(smem_raw)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
   uint32_t* err = &g_kv_attention_error;

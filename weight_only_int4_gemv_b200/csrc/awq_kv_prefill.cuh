@@ -101,12 +101,14 @@ __device__ __forceinline__ bool elect_one() {
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-// this warp's 32 lanes x 32 columns, complete after tc_ld_done on the same registers
+// this warp's 32 lanes x 32 columns. The wait is in the same statement: nothing may read r before it, and as a
+// statement of its own with r as operands it costs a register move each.
 __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
       "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,"
-      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+      "%16,%17,%18,%19,%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];\n\t"
+      "tcgen05.wait::ld.sync.aligned;"
       : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
         "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]),
         "=r"(r[17]), "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]),
@@ -114,32 +116,14 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
       : "r"(a)
       : "memory");
 }
-// (the registers are its operands, so that nothing reads them before it)
-__device__ __forceinline__ void tc_ld_done(uint32_t (&r)[32]) {
-  asm volatile("tcgen05.wait::ld.sync.aligned;"
-               : "+r"(r[0]), "+r"(r[1]), "+r"(r[2]), "+r"(r[3]), "+r"(r[4]), "+r"(r[5]), "+r"(r[6]), "+r"(r[7]),
-                 "+r"(r[8]), "+r"(r[9]), "+r"(r[10]), "+r"(r[11]), "+r"(r[12]), "+r"(r[13]), "+r"(r[14]), "+r"(r[15]),
-                 "+r"(r[16]), "+r"(r[17]), "+r"(r[18]), "+r"(r[19]), "+r"(r[20]), "+r"(r[21]), "+r"(r[22]),
-                 "+r"(r[23]), "+r"(r[24]), "+r"(r[25]), "+r"(r[26]), "+r"(r[27]), "+r"(r[28]), "+r"(r[29]),
-                 "+r"(r[30]), "+r"(r[31])
-               :
-               : "memory");
-}
-// two fp32 operations in one instruction
-__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
-      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+__device__ __forceinline__ float max3(float a, float b, float c) {
+  float d;
+  asm("max.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
-__device__ __forceinline__ float2 add2(float2 a, float2 b) {
-  float2 d;
-  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
-      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
-      : "=f"(d.x), "=f"(d.y)
-      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+__device__ __forceinline__ float min3(float a, float b, float c) {
+  float d;
+  asm("min.f32 %0, %1, %2, %3;" : "=f"(d) : "f"(a), "f"(b), "f"(c));
   return d;
 }
 // 32 bytes to a 32-byte-aligned address
@@ -244,21 +228,28 @@ __device__ __forceinline__ void mask32(uint32_t (&r)[32], int hi, int lo, int sk
     if (!((k <= hi) & ((k >= lo) | (k < sk)))) r[k] = __float_as_uint(value);
 }
 
-template <class Op>
-__device__ __forceinline__ float largest16(const uint32_t* r, Op op) {
-  float a = op(__uint_as_float(r[0]), __uint_as_float(r[1])), b = op(__uint_as_float(r[2]), __uint_as_float(r[3]));
-#pragma unroll
-  for (int e = 4; e < 16; e += 4) {
-    a = op(a, op(__uint_as_float(r[e]), __uint_as_float(r[e + 1])));
-    b = op(b, op(__uint_as_float(r[e + 2]), __uint_as_float(r[e + 3])));
-  }
-  return op(a, b);
+// Largest (smallest) of 16.
+template <class Op3>
+__device__ __forceinline__ float extreme16(const uint32_t* r, Op3 op) {
+  auto f = [&](int i) { return __uint_as_float(r[i]); };
+  const float a = op(f(0), f(1), f(2)), b = op(f(3), f(4), f(5)), c = op(f(6), f(7), f(8)), d = op(f(9), f(10), f(11));
+  return op(op(a, b, f(12)), op(c, d, f(13)), op(f(14), f(15), f(15)));
 }
 
-// A bounded wait in few instructions (it is inlined in many places).
+// A bounded wait in few instructions: it is inlined in many places, and a
+// warp that polls shares its scheduler with one that works.
 __device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
   for (long long t0 = 0;;) {
-    if (mbar_try_wait_sleep(bar, parity)) return true;
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t@q bra POLL_%=;\n"
+        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
     const long long t = clock64();
     if (t0 == 0) t0 = t;
     if (t - t0 > kWaitCycles || *abort) {
@@ -277,7 +268,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   constexpr uint32_t kIdescS = (1u << 4) | (uint32_t(kTile >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
   constexpr uint32_t kIdescO = (1u << 4) | (1u << 16) | (uint32_t(D >> 3) << 17) | (uint32_t(kTile >> 4) << 24);
   extern __shared__ uint8_t smem_raw[];
-  Sh& sh = *reinterpret_cast<Sh*>((reinterpret_cast<uintptr_t>(smem_raw) + 1023) & ~uintptr_t(1023));
+  // (an offset from the array, not a rounded address: the compiler then knows it is shared memory)
+  Sh& sh = *reinterpret_cast<Sh*>(smem_raw + ((0u - smem_u32(smem_raw)) & 1023u));
   const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
   volatile int* abort = &sh.abort;
   uint32_t* err = &g_kv_attention_error;
@@ -366,18 +358,17 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
 #pragma unroll 1
         for (int c = 0; c < kTile / 32; ++c) {
           uint32_t r[32];
-          tc_ld32(ts + c * 32, r);
           const float a0 = factor * __shfl_sync(0xffffffffu, ks, 2 * c), a1 = factor * __shfl_sync(0xffffffffu, ks, 2 * c + 1);
           const float b0 = __shfl_sync(0xffffffffu, lv, 2 * c), b1 = __shfl_sync(0xffffffffu, lv, 2 * c + 1);
-          tc_ld_done(r);
+          tc_ld32(ts + c * 32, r);
           if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, p.scale_log2 < 0.0f ? INFINITY : -INFINITY);
           float t0, t1;
           if (p.scale_log2 >= 0.0f) {
-            t0 = largest16(r, [](float u, float v) { return fmaxf(u, v); });
-            t1 = largest16(r + 16, [](float u, float v) { return fmaxf(u, v); });
+            t0 = extreme16(r, max3);
+            t1 = extreme16(r + 16, max3);
           } else {
-            t0 = largest16(r, [](float u, float v) { return fminf(u, v); });
-            t1 = largest16(r + 16, [](float u, float v) { return fminf(u, v); });
+            t0 = extreme16(r, min3);
+            t1 = extreme16(r + 16, min3);
           }
           top = fmaxf(top, fmaxf(fmaf(t0, a0, b0), fmaf(t1, a1, b1)));
         }
@@ -392,7 +383,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             for (int c = 0; c < D / 32; ++c) {
               uint32_t r[32];
               tc_ld32(to + c * 32, r);
-              tc_ld_done(r);
 #pragma unroll
               for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
               tc_st32(to + c * 32, r);
@@ -406,35 +396,29 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
 #pragma unroll 1
         for (int c = 0; c < kTile / 32; ++c) {
           uint32_t r[32], pk[16];
-          tc_ld32(ts + c * 32, r);
-          float2 fa[2], fb[2], part[2];
-          float is[2];
+          float fa[2], fb[2], is[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            const float a = factor * __shfl_sync(0xffffffffu, ks, 2 * c + h);
-            const float b = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
+            fa[h] = factor * __shfl_sync(0xffffffffu, ks, 2 * c + h);
+            fb[h] = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
             is[h] = __shfl_sync(0xffffffffu, iv, 2 * c + h);
-            fa[h] = make_float2(a, a);
-            fb[h] = make_float2(b, b);
-            part[h] = make_float2(0.0f, 0.0f);
           }
-          tc_ld_done(r);
+          tc_ld32(ts + c * 32, r);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const int h = e >> 4;
-            float2 t = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])), fa[h], fb[h]);
-            r[e] = __float_as_uint(t.x);
-            r[e + 1] = __float_as_uint(t.y);
-          }
+          for (int e = 0; e < 32; ++e)
+            r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), fa[e >> 4], fb[e >> 4]));
           if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, -INFINITY);
 #pragma unroll
-          for (int e = 0; e < 32; e += 2) {
-            const float2 w = make_float2(exp2_fast(__uint_as_float(r[e])), exp2_fast(__uint_as_float(r[e + 1])));
-            part[e >> 4] = add2(part[e >> 4], w);
-            pk[e / 2] = Half16<__half>::pack(w.x, w.y);
+          for (int h = 0; h < 2; ++h) {
+            float w[16];
+#pragma unroll
+            for (int e = 0; e < 16; ++e) w[e] = exp2_fast(__uint_as_float(r[16 * h + e]));
+            l = fmaf(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])) +
+                         (((w[8] + w[9]) + (w[10] + w[11])) + ((w[12] + w[13]) + (w[14] + w[15]))),
+                     is[h], l);
+#pragma unroll
+            for (int e = 0; e < 8; ++e) pk[8 * h + e] = Half16<__half>::pack(w[2 * e], w[2 * e + 1]);
           }
-          l = fmaf(part[0].x + part[0].y, is[0], l);
-          l = fmaf(part[1].x + part[1].y, is[1], l);
           tc_st16(ts + c * 16, pk);
         }
         tc_wait_st();
@@ -462,7 +446,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           uint32_t r[32];
           if (pv > 0) {
             tc_ld32(to + c * 32, r);
-            tc_ld_done(r);
           } else {
 #pragma unroll
             for (int e = 0; e < 32; ++e) r[e] = 0;
@@ -506,7 +489,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   } else if (warp < 12) {
     // ---------------------------------------------------------- codes to fp16
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
+    // A thread takes 16-byte chunk k of the rows r0, r0 + kRowStep, ...: 16 channels, chunks 2k and 2k + 1 (mod 8) of
+    // its panel's row. Eight lanes read eight chunks at once, and write to eight different ones: with two panels,
+    // lanes 4-7 take the row beside lanes 0-3's, whose chunks the swizzle puts on the other places.
     const int tid = threadIdx.x - 8 * 32;
+    constexpr int CPR = D / 16, kRowStep = 128 / CPR;
+    const int k = tid % CPR, r0 = D == 128 ? (tid >> 3) ^ (k >> 2) : tid / CPR;
+    const int raw_at = r0 * D + k * 16, half_at = (k >> 2) * (kTile * 128) + r0 * 128;
+    const int c0 = ((2 * (k & 3)) ^ (r0 & 7)) << 4, c1 = ((2 * (k & 3) + 1) ^ (r0 & 7)) << 4;
     int n = 0;                                  // tiles of codes converted
     for (int it = 0;; ++it) {
       const int mi = it % kMetaSlots;
@@ -518,30 +508,24 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
       if (!(flags & (kAct0 | kAct1))) continue;  // a tile without keys
       bool ok = true;
+#pragma unroll 1
       for (int kv = 0; kv < 2; ++kv, ++n) {
         const int rs = n % kRawSlots, hs = n % kHalfSlots;
         if (!wait(&sh.raw_full[rs], (n / kRawSlots) & 1) || !wait(&sh.half_empty[hs], ((n / kHalfSlots) & 1) ^ 1)) {
           ok = false;
           break;
         }
-        constexpr int CPR = D / 16;             // raw 16-byte chunks of a key
-        const uint8_t* raw = sh.raw[rs];
-        uint8_t* out = sh.half[hs];
+        const uint8_t* raw = sh.raw[rs] + raw_at;
+        uint8_t* half = sh.half[hs] + half_at;
 #pragma unroll
-        for (int i = 0; i < kTile * CPR / 128; ++i) {
-          const int c = i * 128 + tid, r = c / CPR, k = c % CPR;
-          uint4 w = *reinterpret_cast<const uint4*>(raw + c * 16);
+        for (int i = 0; i < kTile / kRowStep; ++i) {
+          uint4 w = *reinterpret_cast<const uint4*>(raw + i * kRowStep * D);
           // e4m3 bytes behind the end may be NaN, which a weight of 0 does not silence
-          if (FMT == AWQ_KV_E4M3 && r >= valid) w = make_uint4(0, 0, 0, 0);
+          if (FMT == AWQ_KV_E4M3 && r0 + i * kRowStep >= valid) w = make_uint4(0, 0, 0, 0);
           uint4 a, b;
           widen16<FMT>(w, a, b);
-          // chunks 2k', 2k'+1 of the row's panel; the second panel's odd one first, so that a row's writes
-          // fall on different banks
-          uint8_t* dst = out + (k >> 2) * (kTile * 128) + r * 128;
-          const int odd = k >> 2;
-          const int c0 = 2 * (k & 3) + odd, c1 = 2 * (k & 3) + 1 - odd;
-          *reinterpret_cast<uint4*>(dst + ((c0 ^ (r & 7)) << 4)) = odd ? b : a;
-          *reinterpret_cast<uint4*>(dst + ((c1 ^ (r & 7)) << 4)) = odd ? a : b;
+          *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c0) = a;
+          *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c1) = b;
         }
         fence_proxy_async_smem();
         __syncwarp();
@@ -736,8 +720,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
     // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
-    uint32_t q_ph[2] = {0, 0}, p_ph[2] = {0, 0}, of_ph[2] = {0, 0};
-    int segs[2] = {0, 0};                        // segments the row tile's O was used in
+    // bit x: parity of the row tile's next q rows, weights, free O; whether its O was used before (bits, because an
+    // array indexed by x would live in local memory)
+    uint32_t q_ph = 0, p_ph = 0, of_ph = 0, used_o = 0;
     int n = 0;                                   // code tiles taken
     bool ok = true;
     auto commit = [&](uint64_t* bar) {
@@ -747,8 +732,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // S = Q K^T of row tile x
     auto product_s = [&](int x, int hs, int flags) {
       if (flags & (x ? kBegin1 : kBegin0)) {
-        if (!wait(&sh.q_full[x], q_ph[x])) return false;
-        q_ph[x] ^= 1;
+        if (!wait(&sh.q_full[x], (q_ph >> x) & 1)) return false;
+        q_ph ^= 1u << x;
       }
       tc_after();
       const uint64_t q = desc_k(smem_u32(sh.q[x])), k = desc_k(smem_u32(sh.half[hs]));
@@ -767,13 +752,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       return true;
     };
     auto product_o = [&](int x, int hs, int flags) {
-      if (!wait(&sh.p_ready[x], p_ph[x])) return false;
-      p_ph[x] ^= 1;
+      if (!wait(&sh.p_ready[x], (p_ph >> x) & 1)) return false;
+      p_ph ^= 1u << x;
       if (flags & (x ? kBegin1 : kBegin0)) {
-        if (segs[x]++) {
-          if (!wait(&sh.o_free[x], of_ph[x])) return false;
-          of_ph[x] ^= 1;
+        if ((used_o >> x) & 1) {
+          if (!wait(&sh.o_free[x], (of_ph >> x) & 1)) return false;
+          of_ph ^= 1u << x;
         }
+        used_o |= 1u << x;
       }
       tc_after();
       const uint64_t v = desc_mn(smem_u32(sh.half[hs]));
@@ -801,42 +787,36 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         if (f & (kAct0 | kAct1)) return f;
       }
     };
-    int cur = take();
-    if (cur > 0) {
-      const int hs = n % kHalfSlots;
-      ok = wait(&sh.half_full[hs], (n / kHalfSlots) & 1);
-      for (int x = 0; x < 2 && ok; ++x)
-        if (cur & (x ? kAct1 : kAct0)) ok = product_s(x, hs, cur);
-      if (ok) commit(&sh.half_empty[hs]);
-      ++n;
-    }
-    while (ok && cur > 0) {
+    // A round: O of the tile at hand (none in the first round), S of the next (none in the last). Within a segment
+    // in the order O0, S0, O1, S1; where the next tile begins one, both O first: its q rows may still be on the way.
+    for (int cur = 0;;) {
       const int next = take();
-      if (next < 0) break;
-      const int vs = n % kHalfSlots, ks = (n + 1) % kHalfSlots;
-      const uint32_t v_ph = (n / kHalfSlots) & 1, k_ph = ((n + 1) / kHalfSlots) & 1;
-      n += 2;
-      if (!(ok = wait(&sh.half_full[vs], v_ph))) break;
-      // within a segment S0 of the next tile goes between the two O products; at its end both come first
-      const bool same = next > 0 && !(next & kBegin);
+      if (next < 0 || (next == 0 && cur == 0)) break;
+      const int vs = n % kHalfSlots;
+      if (cur) {
+        ok = wait(&sh.half_full[vs], (n / kHalfSlots) & 1);
+        ++n;
+      }
+      const int ks = n % kHalfSlots;
+      const uint32_t k_ph = (n / kHalfSlots) & 1;
+      const bool same = !(next & kBegin);
       bool have_k = false;
-      for (int x = 0; x < 2 && ok; ++x) {
-        if (cur & (x ? kAct1 : kAct0)) ok = product_o(x, vs, cur);
-        if (ok && x == 1) commit(&sh.half_empty[vs]);
-        if (ok && same && (next & (x ? kAct1 : kAct0))) {
+#pragma unroll 1
+      for (int step = 0; step < 4 && ok; ++step) {
+        const int x = same ? step >> 1 : step & 1;
+        const int bit = x ? kAct1 : kAct0;
+        if (!(same ? step & 1 : step >> 1)) {
+          if (cur & bit) ok = product_o(x, vs, cur);
+          if (ok && cur && x == 1) commit(&sh.half_empty[vs]);
+        } else if (next & bit) {
           if (!have_k) ok = wait(&sh.half_full[ks], k_ph);
           have_k = true;
           if (ok) ok = product_s(x, ks, next);
         }
       }
-      if (ok && next > 0) {
-        if (!same) {
-          ok = wait(&sh.half_full[ks], k_ph);
-          for (int x = 0; x < 2 && ok; ++x)
-            if (next & (x ? kAct1 : kAct0)) ok = product_s(x, ks, next);
-        }
-        if (ok) commit(&sh.half_empty[ks]);
-      }
+      if (!ok || next == 0) break;
+      commit(&sh.half_empty[ks]);
+      ++n;
       cur = next;
     }
     // everything issued has finished before tensor memory is given back
