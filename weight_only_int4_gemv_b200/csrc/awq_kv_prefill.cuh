@@ -103,6 +103,16 @@ __device__ __forceinline__ bool elect_one() {
 }
 // this warp's 32 lanes x 32 columns. The wait is in the same statement: nothing may read r before it, and as a
 // statement of its own with r as operands it costs a register move each.
+__device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
+  asm volatile(
+      "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
+      "{%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}"
+      ", [%16];\n\ttcgen05.wait::ld.sync.aligned;"
+      : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), 
+        "=r"(r[8]), "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15])
+      : "r"(a)
+      : "memory");
+}
 __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x32.b32 "
@@ -115,6 +125,23 @@ __device__ __forceinline__ void tc_ld32(uint32_t a, uint32_t (&r)[32]) {
         "=r"(r[25]), "=r"(r[26]), "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
       : "r"(a)
       : "memory");
+}
+// two fp32 operations in one instruction
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, c, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\tmov.b64 c, {%6, %7};\n\t"
+      "fma.rn.f32x2 d, a, b, c;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+  return d;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+  float2 d;
+  asm("{\n\t.reg .b64 a, b, d;\n\tmov.b64 a, {%2, %3};\n\tmov.b64 b, {%4, %5};\n\t"
+      "add.rn.f32x2 d, a, b;\n\tmov.b64 {%0, %1}, d;\n\t}"
+      : "=f"(d.x), "=f"(d.y)
+      : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+  return d;
 }
 __device__ __forceinline__ float max3(float a, float b, float c) {
   float d;
@@ -219,13 +246,6 @@ template <int FMT>
 __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
   a = make_uint4(code_pair<FMT, 0>(c.x), code_pair<FMT, 2>(c.x), code_pair<FMT, 0>(c.y), code_pair<FMT, 2>(c.y));
   b = make_uint4(code_pair<FMT, 0>(c.z), code_pair<FMT, 2>(c.z), code_pair<FMT, 0>(c.w), code_pair<FMT, 2>(c.w));
-}
-
-// Column k of 32 is visible if k <= hi and (k >= lo or k < sk); the others get `value`.
-__device__ __forceinline__ void mask32(uint32_t (&r)[32], int hi, int lo, int sk, float value) {
-#pragma unroll
-  for (int k = 0; k < 32; ++k)
-    if (!((k <= hi) & ((k >= lo) | (k < sk)))) r[k] = __float_as_uint(value);
 }
 
 // Largest (smallest) of 16.
@@ -352,25 +372,44 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         tc_after();
         // (written before the row tile's first S was computed)
         if (std::is_same<T, __nv_bfloat16>::value && pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];
-        // Two passes over S, each a rolled loop of 32 columns (straight code for a whole tile misses the
-        // instruction cache). First the row's largest logit.
+        const bool flip = p.scale_log2 < 0.0f;
+        // t = a S + log2(s_v); |a| stays above 0, so that an infinite S is an infinite t (2^-100 S is no logit)
+        auto block_a = [&](int b) {
+          const float a = fmaxf(fabsf(factor) * __shfl_sync(0xffffffffu, ks, b), 7.888609052210118e-31f);
+          return flip ? -a : a;
+        };
+        if (!all) {
+          // masked columns of S become the infinity that a's sign takes to -inf
+#pragma unroll 1
+          for (int c = 0; c < kTile / 32; ++c) {
+            uint32_t r[32];
+            tc_ld32(ts + c * 32, r);
+            const int h = hi - 32 * c, lw = lo - 32 * c, s = sk - 32 * c;
+#pragma unroll
+            for (int k = 0; k < 32; ++k)
+              if (!((k <= h) & ((k >= lw) | (k < s)))) r[k] = flip ? 0x7f800000u : 0xff800000u;
+            tc_st32(ts + c * 32, r);
+          }
+          tc_wait_st();
+        }
+        // Two passes over S, each a short rolled loop: straight code for a whole tile lives on instruction cache
+        // misses. The largest logit: per block the extreme of S, then its t.
         float top = -INFINITY;
 #pragma unroll 1
         for (int c = 0; c < kTile / 32; ++c) {
           uint32_t r[32];
-          const float a0 = factor * __shfl_sync(0xffffffffu, ks, 2 * c), a1 = factor * __shfl_sync(0xffffffffu, ks, 2 * c + 1);
+          const float a0 = block_a(2 * c), a1 = block_a(2 * c + 1);
           const float b0 = __shfl_sync(0xffffffffu, lv, 2 * c), b1 = __shfl_sync(0xffffffffu, lv, 2 * c + 1);
           tc_ld32(ts + c * 32, r);
-          if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, p.scale_log2 < 0.0f ? INFINITY : -INFINITY);
-          float t0, t1;
-          if (p.scale_log2 >= 0.0f) {
-            t0 = extreme16(r, max3);
-            t1 = extreme16(r + 16, max3);
+          float e0, e1;
+          if (flip) {
+            e0 = extreme16(r, min3);
+            e1 = extreme16(r + 16, min3);
           } else {
-            t0 = extreme16(r, min3);
-            t1 = extreme16(r + 16, min3);
+            e0 = extreme16(r, max3);
+            e1 = extreme16(r + 16, max3);
           }
-          top = fmaxf(top, fmaxf(fmaf(t0, a0, b0), fmaf(t1, a1, b1)));
+          top = max3(top, fmaf(e0, a0, b0), fmaf(e1, a1, b1));
         }
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float raised = fmaxf(m, top);
@@ -380,44 +419,42 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 32; ++c) {
-              uint32_t r[32];
-              tc_ld32(to + c * 32, r);
+            for (int c = 0; c < D / 16; ++c) {
+              uint32_t y[16];
+              tc_ld16(to + c * 16, y);
 #pragma unroll
-              for (int e = 0; e < 32; ++e) r[e] = __float_as_uint(__uint_as_float(r[e]) * f);
-              tc_st32(to + c * 32, r);
+              for (int e = 0; e < 16; ++e) y[e] = __float_as_uint(__uint_as_float(y[e]) * f);
+              tc_st16(to + c * 16, y);
             }
           }
           l *= f;
           m = raised;
         }
-        // Then the weights, which take the place of S columns already read.
+        // The weights, over the S columns.
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
         for (int c = 0; c < kTile / 32; ++c) {
           uint32_t r[32], pk[16];
-          float fa[2], fb[2], is[2];
+          float a[2], d[2], is[2];
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
-            fa[h] = factor * __shfl_sync(0xffffffffu, ks, 2 * c + h);
-            fb[h] = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
+            a[h] = block_a(2 * c + h);
+            d[h] = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
             is[h] = __shfl_sync(0xffffffffu, iv, 2 * c + h);
           }
           tc_ld32(ts + c * 32, r);
 #pragma unroll
-          for (int e = 0; e < 32; ++e)
-            r[e] = __float_as_uint(fmaf(__uint_as_float(r[e]), fa[e >> 4], fb[e >> 4]));
-          if (!all) mask32(r, hi - 32 * c, lo - 32 * c, sk - 32 * c, -INFINITY);
-#pragma unroll
           for (int h = 0; h < 2; ++h) {
-            float w[16];
+            float2 part = make_float2(0.0f, 0.0f);
 #pragma unroll
-            for (int e = 0; e < 16; ++e) w[e] = exp2_fast(__uint_as_float(r[16 * h + e]));
-            l = fmaf(((w[0] + w[1]) + (w[2] + w[3])) + ((w[4] + w[5]) + (w[6] + w[7])) +
-                         (((w[8] + w[9]) + (w[10] + w[11])) + ((w[12] + w[13]) + (w[14] + w[15]))),
-                     is[h], l);
-#pragma unroll
-            for (int e = 0; e < 8; ++e) pk[8 * h + e] = Half16<__half>::pack(w[2 * e], w[2 * e + 1]);
+            for (int e = 16 * h; e < 16 * h + 16; e += 2) {
+              const float2 t = fma2(make_float2(__uint_as_float(r[e]), __uint_as_float(r[e + 1])),
+                                    make_float2(a[h], a[h]), make_float2(d[h], d[h]));
+              const float2 w = make_float2(exp2_fast(t.x), exp2_fast(t.y));
+              part = add2(part, w);
+              pk[e / 2] = Half16<__half>::pack(w.x, w.y);
+            }
+            l = fmaf(part.x + part.y, is[h], l);
           }
           tc_st16(ts + c * 16, pk);
         }
@@ -517,7 +554,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         }
         const uint8_t* raw = sh.raw[rs] + raw_at;
         uint8_t* half = sh.half[hs] + half_at;
-#pragma unroll
+#pragma unroll 4
         for (int i = 0; i < kTile / kRowStep; ++i) {
           uint4 w = *reinterpret_cast<const uint4*>(raw + i * kRowStep * D);
           // e4m3 bytes behind the end may be NaN, which a weight of 0 does not silence
@@ -720,25 +757,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
     // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
     asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
+    if (elect_one()) {
+    auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_small(bar, parity, abort, err); };
     // bit x: parity of the row tile's next q rows, weights, free O; whether its O was used before (bits, because an
     // array indexed by x would live in local memory)
     uint32_t q_ph = 0, p_ph = 0, of_ph = 0, used_o = 0;
     int n = 0;                                   // code tiles taken
     bool ok = true;
-    auto commit = [&](uint64_t* bar) {
-      if (elect_one()) tc_commit(bar);
-      __syncwarp();
-    };
     // S = Q K^T of row tile x
     auto product_s = [&](int x, int hs, int flags) {
       if (flags & (x ? kBegin1 : kBegin0)) {
-        if (!wait(&sh.q_full[x], (q_ph >> x) & 1)) return false;
+        if (!wait1(&sh.q_full[x], (q_ph >> x) & 1)) return false;
         q_ph ^= 1u << x;
       }
       tc_after();
       const uint64_t q = desc_k(smem_u32(sh.q[x])), k = desc_k(smem_u32(sh.half[hs]));
       const uint32_t d = tmem + x * kTile;
-      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < D / 16; ++i) {
           constexpr int kStep = 32 >> 4;         // 16 channels, in the descriptor's units
@@ -747,16 +781,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         }
         tc_commit(&sh.s_full[x]);
         if (flags & (x ? kEnd1 : kEnd0)) tc_commit(&sh.q_free[x]);
-      }
-      __syncwarp();
       return true;
     };
     auto product_o = [&](int x, int hs, int flags) {
-      if (!wait(&sh.p_ready[x], (p_ph >> x) & 1)) return false;
+      if (!wait1(&sh.p_ready[x], (p_ph >> x) & 1)) return false;
       p_ph ^= 1u << x;
       if (flags & (x ? kBegin1 : kBegin0)) {
         if ((used_o >> x) & 1) {
-          if (!wait(&sh.o_free[x], (of_ph >> x) & 1)) return false;
+          if (!wait1(&sh.o_free[x], (of_ph >> x) & 1)) return false;
           of_ph ^= 1u << x;
         }
         used_o |= 1u << x;
@@ -765,12 +797,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const uint64_t v = desc_mn(smem_u32(sh.half[hs]));
       const uint32_t more = (flags & (x ? kBegin1 : kBegin0)) ? 0u : 1u;
       const uint32_t d = tmem + 2 * kTile + x * D, w = tmem + x * kTile;
-      if (elect_one()) {
 #pragma unroll
         for (int i = 0; i < kTile / 16; ++i) tc_mma_ts(d, w + i * 8, v + i * (2048 >> 4), kIdescO, i > 0 ? 1u : more);
         tc_commit(&sh.o_full[x]);
-      }
-      __syncwarp();
       return true;
     };
     // the flags of the next tile with keys (0: none left)
@@ -778,12 +807,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     auto take = [&]() -> int {
       for (;;) {
         const int mi = it % kMetaSlots;
-        if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) return -1;
+        if (!wait1(&sh.meta_full[mi], (it / kMetaSlots) & 1)) return -1;
         const int f = sh.meta[mi].flags;
         if (f & kStop) return 0;
         ++it;
-        __syncwarp();
-        if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
+        mbar_arrive(&sh.meta_empty[mi]);
         if (f & (kAct0 | kAct1)) return f;
       }
     };
@@ -794,7 +822,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       if (next < 0 || (next == 0 && cur == 0)) break;
       const int vs = n % kHalfSlots;
       if (cur) {
-        ok = wait(&sh.half_full[vs], (n / kHalfSlots) & 1);
+        ok = wait1(&sh.half_full[vs], (n / kHalfSlots) & 1);
         ++n;
       }
       const int ks = n % kHalfSlots;
@@ -807,21 +835,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         const int bit = x ? kAct1 : kAct0;
         if (!(same ? step & 1 : step >> 1)) {
           if (cur & bit) ok = product_o(x, vs, cur);
-          if (ok && cur && x == 1) commit(&sh.half_empty[vs]);
+          if (ok && cur && x == 1) tc_commit(&sh.half_empty[vs]);
         } else if (next & bit) {
-          if (!have_k) ok = wait(&sh.half_full[ks], k_ph);
+          if (!have_k) ok = wait1(&sh.half_full[ks], k_ph);
           have_k = true;
           if (ok) ok = product_s(x, ks, next);
         }
       }
       if (!ok || next == 0) break;
-      commit(&sh.half_empty[ks]);
+      tc_commit(&sh.half_empty[ks]);
       ++n;
       cur = next;
     }
     // everything issued has finished before tensor memory is given back
-    commit(&sh.done);
+    tc_commit(&sh.done);
     wait_sleep_teardown(&sh.done, 0);
+    }
   } else {
     // ------------------------------------------------------------------ q rows
     // Each warp brings 64 rows of both tiles: asynchronous copies into their swizzled places, then, for bf16, a
