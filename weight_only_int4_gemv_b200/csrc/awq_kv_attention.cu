@@ -78,6 +78,9 @@ struct Join {
   int32_t pad[2];
 };
 
+// The first key in the window of position p.
+__device__ __forceinline__ int window_start(int p, int window) { return window && p >= window ? p - window + 1 : 0; }
+
 // The keys that a sequence's rows may see: sink tiles, then the tiles from w0.
 struct Span {
   int tiles, sink_tiles, w0, row_tiles;
@@ -90,7 +93,7 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, const Seq& s) 
     a.tiles = a.sink_tiles = a.w0 = a.row_tiles = 0;
     return a;
   }
-  const int low = p.window ? max(0, s.past - p.window + 1) : 0;
+  const int low = window_start(s.past, p.window);
   a.w0 = min(low, s.len) / kBlock;
   a.sink_tiles = p.window ? min((min(p.sinks, low) + kBlock - 1) / kBlock, a.w0) : 0;
   a.tiles = max(a.sink_tiles + (s.len + kBlock - 1) / kBlock - a.w0, 1);   // one for a row that sees nothing
@@ -818,8 +821,9 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   p.v_scales = cache->v_scales;
   p.scale_stride = cache->scale_stride;
   p.scale_log2 = scale * kLog2e;
-  p.window = window;
-  p.sinks = window ? sinks : 0;
+  // A window that no sequence can outgrow is none (and the kernels' differences of positions stay in 32 bits).
+  p.window = int64_t(window) >= int64_t(batch->max_pages) * cache->page_size ? 0 : window;
+  p.sinks = p.window ? sinks : 0;
   p.group = n_q_heads / cache->n_kv_heads;
   p.n_kv_heads = cache->n_kv_heads;
   p.joins = static_cast<Join*>(workspace);

@@ -13,29 +13,32 @@
 // and the softmax of one row tile runs while the other's products do.
 //
 // Warps:
-//   0-3, 4-7  softmax of row tile 0 / 1: one row per thread. S comes from
-//             tensor memory, the weights go back over it as fp16 (the A
-//             operand of the second product). m is only raised when a logit
-//             passes it by more than 8 (log2 units), so the outputs in tensor
-//             memory are almost never rescaled and a tile needs one pass.
-//   8-11      codes to fp16 (exact) in the tensor core's 128-byte-swizzled
-//             layout: keys K-major, values as they lie (MN-major).
-//   12        pages, scales and the tiles' descriptions, TMA of the codes.
-//   13        the products: S0 = Q0 K^T, S1 = Q1 K^T, O0 += P0 V, O1 += P1 V.
-//   14, 15    q rows to fp16, a segment ahead.
-// Registers move from the last two warpgroups to the softmax's.
-// Tensor memory: S0, S1 (128 columns each; P lies over its S), O0, O1.
+//   0-15      softmax: a thread has half a row (64 of a tile's keys) of row
+//             tile 0 (warps 0-3, 8-11) or 1 (4-7, 12-15); the halves exchange
+//             their largest logits through shared memory. S comes from tensor
+//             memory, the weights go back over it as fp16 (the A operand of
+//             the second product). m is only raised when a logit passes it by
+//             more than 8 (log2 units), so the outputs in tensor memory are
+//             almost never rescaled.
+//   16-19     codes to fp16 (exact) in the tensor core's 128-byte-swizzled
+//             layout: keys K-major, values as they lie (MN-major); the
+//             blocks' constants.
+//   20        pages, scales and the tiles' descriptions, TMA of the codes.
+//   21        the products: S0 = Q0 K^T, S1 = Q1 K^T, O0 += P0 V, O1 += P1 V.
+//   22, 23    q rows to fp16, a segment ahead.
+// Tensor memory: S0, S1 (128 columns each; a half row's P lies over its S), O0, O1.
 //
 // Work is laid end to end in units of 128 keys and cut evenly over the CTAs,
 // as for few rows; split items meet in join_rows_kernel.
 
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
-constexpr int kPreThreads = 16 * 32;
-constexpr int kMoreRegs = 144, kLessRegs = 112;   // 2 * 144 + 2 * 112 = 4 * 128, what the launch holds
+constexpr int kSoftmaxWarps = 16, kWidenWarps = 4;
+constexpr int kPreThreads = (kSoftmaxWarps + kWidenWarps + 4) * 32;
 // What a segment costs beyond its tiles (q rows, first S, epilogue), in tiles: the schedule counts every item as
 // that much longer.
 constexpr int kSegmentCost = 2;
+constexpr float kLeastA = 7.888609052210118e-31f;    // 2^-100
 constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
@@ -52,7 +55,8 @@ struct PreMeta {
   int pos, valid, flags;
   int t0, row0, rows, past, head, dest;
   int pad[3];
-  float ks[8], vs[8];
+  float ks[8], vs[8];            // the blocks' scales
+  float a[8], lv[8], iv[8];      // scale log2(e) s_k, log2(s_v), 1 / s_v
 };
 
 template <int D>
@@ -61,7 +65,10 @@ struct PreShared {
   uint8_t half[kHalfSlots][kTile * D * 2];
   uint8_t raw[kRawSlots][kTile * D];
   float factor[kMetaSlots][2][kTile];          // [segment][row tile][row]: a ring of as many segments as tiles
+  float peak[2][2][2][kTile];                  // [tile parity][row tile][half][row]: a half row's largest logit
+  float mass[2][2][kTile];                     // its sum of weights, at a segment's end
   PreMeta meta[kMetaSlots];
+  uint64_t both[2];                            // the halves' exchange
   uint64_t meta_full[kMetaSlots], meta_empty[kMetaSlots];
   uint64_t raw_full[kRawSlots], raw_empty[kRawSlots];
   uint64_t half_full[kHalfSlots], half_empty[kHalfSlots];
@@ -212,7 +219,7 @@ __device__ __forceinline__ Pair pair_of(const AttentionParams& p, const Seq& s, 
       const int p_low = s.past + first / p.group, p_high = s.past + (min(first + kTile, rows) - 1) / p.group;
       if (p_high >= 0) {
         r.hi[x] = p_high / kTile;
-        const int start = p.window ? max(0, p_low - p.window + 1) : 0;
+        const int start = window_start(p_low, p.window);
         r.lo[x] = start / kTile;
         if (x == 0 || hi < 0) low = start;
         hi = max(hi, r.hi[x]);
@@ -296,7 +303,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   if (threadIdx.x == 0) {
     for (int i = 0; i < kMetaSlots; ++i) {
       mbar_init(&sh.meta_full[i], 33);
-      mbar_init(&sh.meta_empty[i], 15);        // all warps but the one that writes it
+      mbar_init(&sh.meta_empty[i], kSoftmaxWarps + kWidenWarps + 3);   // all warps but the one that writes it
     }
     for (int i = 0; i < kRawSlots; ++i) {
       mbar_init(&sh.raw_full[i], 1);
@@ -310,16 +317,17 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       mbar_init(&sh.q_full[x], 2);
       mbar_init(&sh.q_free[x], 1);
       mbar_init(&sh.s_full[x], 1);
-      mbar_init(&sh.p_ready[x], 4);
+      mbar_init(&sh.p_ready[x], kSoftmaxWarps / 2);
+      mbar_init(&sh.both[x], kSoftmaxWarps / 2);
       mbar_init(&sh.o_full[x], 1);
-      mbar_init(&sh.o_free[x], 4);
+      mbar_init(&sh.o_free[x], kSoftmaxWarps / 2);
     }
     mbar_init(&sh.done, 1);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
   }
-  if (warp == 13) {
+  if (warp == kSoftmaxWarps + kWidenWarps + 1) {
     asm volatile("tcgen05.alloc.cta_group::1.sync.aligned.shared::cta.b32 [%0], 512;" ::"r"(smem_u32(&sh.tmem)));
     asm volatile("tcgen05.relinquish_alloc_permit.cta_group::1.sync.aligned;");
   }
@@ -334,15 +342,16 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
   };
 
-  if (warp < 8) {
+  if (warp < kSoftmaxWarps) {
     // -------------------------------------------------------------- softmax
-    asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(kMoreRegs));
-    const int x = warp >> 2, row = threadIdx.x & (kTile - 1);
+    const int x = (warp >> 2) & 1, half = warp >> 3, row = threadIdx.x & (kTile - 1);
     const uint32_t lanes = uint32_t((warp & 3) * 32) << 16;
-    const uint32_t ts = tmem + lanes + x * kTile, to = tmem + lanes + 2 * kTile + x * D;
-    float m = -INFINITY, l = 0.0f, factor = p.scale_log2;
+    // this half's columns of S (its weights lie over the first of them) and of O
+    const uint32_t ts = tmem + lanes + x * kTile + half * (kTile / 2);
+    const uint32_t to = tmem + lanes + 2 * kTile + x * D + half * (D / 2);
+    float m = -INFINITY, l = 0.0f, factor = 1.0f;      // l: of this half
     int pv = 0, p_row = 0, p_low = 0, p_high = 0;      // pv: products into O in this segment
-    uint32_t s_ph = 0, o_ph = 0;                       // parity of the next S, of the next O
+    uint32_t s_ph = 0, o_ph = 0, both_ph = 0;          // parity of the next S, of the next O, of the next exchange
     uint32_t seg = 0;
     for (int it = 0;; ++it) {
       const int mi = it % kMetaSlots;
@@ -363,25 +372,24 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         const int pos = me.pos;
         const bool all = pos + kTile - 1 <= p_low &&
                          (p.window == 0 || pos > p_high - p.window || pos + kTile <= p.sinks);
-        const int hi = p_row - pos, lo = p.window ? hi - p.window + 1 : 0, sk = p.window ? p.sinks - pos : 0;
-        // lane b: the constants of block b
-        const float ks = me.ks[lane & 7], vs = me.vs[lane & 7];
-        const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
+        const int k0 = half * (kTile / 2);             // the first key's column
+        const int hi = p_row - pos - k0, lo = p.window ? hi - p.window + 1 : 0,
+                  sk = p.window ? p.sinks - pos - k0 : 0;
         if (!wait(&sh.s_full[x], s_ph)) break;
         s_ph ^= 1;
         tc_after();
         // (written before the row tile's first S was computed)
-        if (std::is_same<T, __nv_bfloat16>::value && pv == 0) factor = p.scale_log2 * sh.factor[seg % kMetaSlots][x][row];
+        if (std::is_same<T, __nv_bfloat16>::value && pv == 0) factor = sh.factor[seg % kMetaSlots][x][row];
         const bool flip = p.scale_log2 < 0.0f;
         // t = a S + log2(s_v); |a| stays above 0, so that an infinite S is an infinite t (2^-100 S is no logit)
-        auto block_a = [&](int b) {
-          const float a = fmaxf(fabsf(factor) * __shfl_sync(0xffffffffu, ks, b), 7.888609052210118e-31f);
-          return flip ? -a : a;
+        auto block_a = [&](float a) {
+          if constexpr (std::is_same<T, __nv_bfloat16>::value) a = copysignf(fmaxf(fabsf(a * factor), kLeastA), a);
+          return a;
         };
         if (!all) {
           // masked columns of S become the infinity that a's sign takes to -inf
 #pragma unroll 1
-          for (int c = 0; c < kTile / 32; ++c) {
+          for (int c = 0; c < kTile / 64; ++c) {
             uint32_t r[32];
             tc_ld32(ts + c * 32, r);
             const int h = hi - 32 * c, lw = lo - 32 * c, s = sk - 32 * c;
@@ -396,10 +404,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         // misses. The largest logit: per block the extreme of S, then its t.
         float top = -INFINITY;
 #pragma unroll 1
-        for (int c = 0; c < kTile / 32; ++c) {
+        for (int c = 0; c < kTile / 64; ++c) {
           uint32_t r[32];
-          const float a0 = block_a(2 * c), a1 = block_a(2 * c + 1);
-          const float b0 = __shfl_sync(0xffffffffu, lv, 2 * c), b1 = __shfl_sync(0xffffffffu, lv, 2 * c + 1);
+          const int b = half * 4 + 2 * c;
+          const float2 a = *reinterpret_cast<const float2*>(&me.a[b]), lv = *reinterpret_cast<const float2*>(&me.lv[b]);
           tc_ld32(ts + c * 32, r);
           float e0, e1;
           if (flip) {
@@ -409,8 +417,16 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             e0 = extreme16(r, max3);
             e1 = extreme16(r + 16, max3);
           }
-          top = max3(top, fmaf(e0, a0, b0), fmaf(e1, a1, b1));
+          top = max3(top, fmaf(e0, block_a(a.x), lv.x), fmaf(e1, block_a(a.y), lv.y));
         }
+        // (the other half of the row has its own part of S and the same m)
+        float* peak = &sh.peak[o_ph][x][0][row];
+        peak[half * kTile] = top;
+        __syncwarp();
+        if (lane == 0) mbar_arrive(&sh.both[x]);
+        if (!wait(&sh.both[x], both_ph)) break;
+        both_ph ^= 1;
+        top = fmaxf(top, peak[(half ^ 1) * kTile]);
         if (__any_sync(0xffffffffu, top > m + kSlack)) {
           const float raised = fmaxf(m, top);
           const float f = raised == -INFINITY ? 1.0f : exp2_fast(m - raised);
@@ -419,7 +435,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
             tc_after();
 #pragma unroll 1
-            for (int c = 0; c < D / 16; ++c) {
+            for (int c = 0; c < D / 32; ++c) {
               uint32_t y[16];
               tc_ld16(to + c * 16, y);
 #pragma unroll
@@ -433,15 +449,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         // The weights, over the S columns.
         const float base = m == -INFINITY ? 0.0f : m;
 #pragma unroll 1
-        for (int c = 0; c < kTile / 32; ++c) {
+        for (int c = 0; c < kTile / 64; ++c) {
           uint32_t r[32], pk[16];
-          float a[2], d[2], is[2];
-#pragma unroll
-          for (int h = 0; h < 2; ++h) {
-            a[h] = block_a(2 * c + h);
-            d[h] = __shfl_sync(0xffffffffu, lv, 2 * c + h) - base;
-            is[h] = __shfl_sync(0xffffffffu, iv, 2 * c + h);
-          }
+          const int b = half * 4 + 2 * c;
+          const float2 a2 = *reinterpret_cast<const float2*>(&me.a[b]), lv = *reinterpret_cast<const float2*>(&me.lv[b]),
+                       iv = *reinterpret_cast<const float2*>(&me.iv[b]);
+          const float a[2] = {block_a(a2.x), block_a(a2.y)}, d[2] = {lv.x - base, lv.y - base}, is[2] = {iv.x, iv.y};
           tc_ld32(ts + c * 32, r);
 #pragma unroll
           for (int h = 0; h < 2; ++h) {
@@ -470,16 +483,22 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         const bool mine = r0 < me.rows;
         const int gr = me.row0 + r0, dest = me.dest;
         uint16_t* dst = p.out + int64_t(me.t0 + gr / p.group) * p.out_stride +
-                        int64_t(me.head * p.group + gr % p.group) * D;
+                        int64_t(me.head * p.group + gr % p.group) * D + half * (D / 2);
         const bool wide = (reinterpret_cast<uintptr_t>(dst) & 31u) == 0;
         float* part = p.part + int64_t(dest) * (kPairRows * (D + 2));
         if (pv > 0) {
           if (!wait(&sh.o_full[x], o_ph ^ 1)) break;
           tc_after();
+          sh.mass[x][half][row] = l;
+          __syncwarp();
+          if (lane == 0) mbar_arrive(&sh.both[x]);
+          if (!wait(&sh.both[x], both_ph)) break;
+          both_ph ^= 1;
+          l += sh.mass[x][half ^ 1][row];
         }
         const float inv = m == -INFINITY ? 0.0f : __fdiv_rn(1.0f, l);
 #pragma unroll 1
-        for (int c = 0; c < D / 32; ++c) {
+        for (int c = 0; c < D / 64; ++c) {
           uint32_t r[32];
           if (pv > 0) {
             tc_ld32(to + c * 32, r);
@@ -508,11 +527,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
             // four channels of a row together, rows side by side: the lanes' stores are contiguous
 #pragma unroll
             for (int e = 0; e < 32; e += 4)
-              *reinterpret_cast<uint4*>(part + ((c * 8 + e / 4) * kPairRows + r0) * 4) =
+              *reinterpret_cast<uint4*>(part + ((half * (D / 8) + c * 8 + e / 4) * kPairRows + r0) * 4) =
                   make_uint4(r[e], r[e + 1], r[e + 2], r[e + 3]);
           }
         }
-        if (mine && dest >= 0) *reinterpret_cast<float2*>(part + kPairRows * D + 2 * r0) = make_float2(m, l);
+        if (mine && dest >= 0 && half == 0) *reinterpret_cast<float2*>(part + kPairRows * D + 2 * r0) = make_float2(m, l);
         if (pv > 0) {
           tc_before();
           __syncwarp();
@@ -523,13 +542,12 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
     }
-  } else if (warp < 12) {
+  } else if (warp < kSoftmaxWarps + kWidenWarps) {
     // ---------------------------------------------------------- codes to fp16
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     // A thread takes 16-byte chunk k of the rows r0, r0 + kRowStep, ...: 16 channels, chunks 2k and 2k + 1 (mod 8) of
     // its panel's row. Eight lanes read eight chunks at once, and write to eight different ones: with two panels,
     // lanes 4-7 take the row beside lanes 0-3's, whose chunks the swizzle puts on the other places.
-    const int tid = threadIdx.x - 8 * 32;
+    const int tid = threadIdx.x - kSoftmaxWarps * 32;
     constexpr int CPR = D / 16, kRowStep = 128 / CPR;
     const int k = tid % CPR, r0 = D == 128 ? (tid >> 3) ^ (k >> 2) : tid / CPR;
     const int raw_at = r0 * D + k * 16, half_at = (k >> 2) * (kTile * 128) + r0 * 128;
@@ -541,6 +559,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const PreMeta& me = sh.meta[mi];
       const int flags = me.flags, valid = me.valid;
       if (flags & kStop) break;
+      if (tid < 8) {                             // (published with the keys)
+        PreMeta& out = sh.meta[mi];
+        const float a = fmaxf(fabsf(p.scale_log2) * me.ks[tid], kLeastA);
+        out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
+        out.lv[tid] = __log2f(me.vs[tid]);
+        out.iv[tid] = __fdividef(1.0f, me.vs[tid]);
+      }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
       if (!(flags & (kAct0 | kAct1))) continue;  // a tile without keys
@@ -573,9 +598,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       }
       if (!ok) break;
     }
-  } else if (warp == 12) {
+  } else if (warp == kSoftmaxWarps + kWidenWarps) {
     // --------------------------------------------- the schedule, pages, copies
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     int64_t total = 0;
     const Batch& a = p.batch;
     for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
@@ -752,11 +776,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // every copy issued has landed before the CTA's shared memory goes
     for (int i = max(0, n - kRawSlots); i < n; ++i)
       wait_sleep_teardown(&sh.raw_full[i % kRawSlots], (i / kRawSlots) & 1);
-  } else if (warp == 13) {
+  } else if (warp == kSoftmaxWarps + kWidenWarps + 1) {
     // ----------------------------------------------------------- the products
     // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
     // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     if (elect_one()) {
     auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_small(bar, parity, abort, err); };
     // bit x: parity of the row tile's next q rows, weights, free O; whether its O was used before (bits, because an
@@ -798,7 +821,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const uint32_t more = (flags & (x ? kBegin1 : kBegin0)) ? 0u : 1u;
       const uint32_t d = tmem + 2 * kTile + x * D, w = tmem + x * kTile;
 #pragma unroll
-        for (int i = 0; i < kTile / 16; ++i) tc_mma_ts(d, w + i * 8, v + i * (2048 >> 4), kIdescO, i > 0 ? 1u : more);
+        for (int i = 0; i < kTile / 16; ++i) 
+          tc_mma_ts(d, w + (i >> 2) * (kTile / 2) + (i & 3) * 8, v + i * (2048 >> 4), kIdescO, i > 0 ? 1u : more);
         tc_commit(&sh.o_full[x]);
       return true;
     };
@@ -855,9 +879,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // ------------------------------------------------------------------ q rows
     // Each warp brings 64 rows of both tiles: asynchronous copies into their swizzled places, then, for bf16, a
     // turn in place to fp16 over a power of two of the row's largest magnitude.
-    asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(kLessRegs));
     constexpr int CPR = D / 8;                   // 16-byte chunks of a row
-    const int r_first = (warp - 14) * 64;
+    const int r_first = (warp - (kSoftmaxWarps + kWidenWarps + 2)) * 64;
     uint32_t q_ph[2] = {0, 0}, seg = 0;
     int used[2] = {0, 0};
     for (int it = 0;; ++it) {
@@ -941,7 +964,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
 
   tc_before();
   __syncthreads();
-  if (warp == 13) {
+  if (warp == kSoftmaxWarps + kWidenWarps + 1) {
     tc_after();
     asm volatile("tcgen05.dealloc.cta_group::1.sync.aligned.b32 %0, 512;" ::"r"(tmem));
   }
