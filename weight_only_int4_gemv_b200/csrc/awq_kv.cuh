@@ -153,6 +153,12 @@ template <class Count, class Target>
 __device__ __forceinline__ int locate(int n_seqs, int64_t* scratch, Count count, Target target, int64_t* rest,
                                       int64_t* total_out) {
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, warps = blockDim.x >> 5;
+  if (n_seqs == 1) {   // nothing to search: one load's latency instead of a scan
+    const int64_t only = count(0), goal = target(only);
+    *rest = goal;
+    if (total_out) *total_out = only;
+    return goal < only ? 0 : -1;
+  }
   const int run = (n_seqs + blockDim.x - 1) / blockDim.x;
   const int b0 = min(int(threadIdx.x) * run, n_seqs), b1 = min(b0 + run, n_seqs);
   int64_t sum = 0;

@@ -154,42 +154,47 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     if (threadIdx.x == 0) atomicOr(&g_kv_append_error, kErrRange);
     hi = max(p.rope_rows - base, lo);
   }
-  const int page = checked_page(
-      p.batch, p.batch.table[int64_t(b) * p.batch.table_stride + base / p.batch.page_size], &g_kv_append_error);
-  if (page < 0 || hi <= lo) return;
+  if (hi <= lo) return;
+  // The loads that depend on nothing but the sequence go out together: the page's id, the table's rows, the first
+  // task's keys or values.
+  const int id = p.batch.table[int64_t(b) * p.batch.table_stride + base / p.batch.page_size];
   const int t0 = s.t0 + (base - s.past);               // row of the block's token 0 (may lie before t0)
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
-
-  if (p.rope) {
-    for (int i = threadIdx.x; i < (hi - lo) * p.rot; i += kThreads) {
-      const int r = lo + i / p.rot, c = i % p.rot;
-      cs[r * p.rot + c] = p.rope[(base + r) * p.rope_stride + c];
-    }
-    __syncthreads();
-  }
-
   const int l = lane % LPR, sub = lane / LPR;
   const int workers = gridDim.y * kWarps, me = blockIdx.y * kWarps + warp;
-  const int off = base % p.batch.page_size;
-
-  // K and V: one head's block per warp
-  for (int task = me; task < 2 * p.n_kv_heads; task += workers) {
+  const int tasks = 2 * p.n_kv_heads;
+  uint4 raw[PASSES];
+  auto fetch = [&](int task) {                          // K or V rows of one head, zeros around the new ones
     const int which = task >= p.n_kv_heads;
-    const int h = which ? task - p.n_kv_heads : task;
-    const uint16_t* src = (which ? p.v : p.k) + int64_t(t0) * (which ? p.v_stride : p.k_stride) + h * D + 8 * l;
     const int64_t stride = which ? p.v_stride : p.k_stride;
-    uint8_t* codes = p.pages[which] + int64_t(page) * p.page_stride +
-                     (int64_t(h) * p.batch.page_size + off) * D + 8 * l;
-    float* scale = p.scales[which] + int64_t(page) * p.scale_stride + h * (p.batch.page_size / kBlock) + off / kBlock;
-    float x[PASSES][8];
+    const uint16_t* src = (which ? p.v : p.k) + int64_t(t0) * stride + (which ? task - p.n_kv_heads : task) * D + 8 * l;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
       const int r = i * RPP + sub;
-      uint4 raw = make_uint4(0, 0, 0, 0);
-      if (r >= lo && r < hi) raw = *reinterpret_cast<const uint4*>(src + r * stride);
-      unpack8<T>(raw, x[i]);
+      raw[i] = r >= lo && r < hi ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0, 0, 0, 0);
     }
+  };
+  if (me < tasks) fetch(me);
+  if (p.rope) {
+    for (int r = lo + warp; r < hi; r += kWarps)
+      for (int c = lane; c < p.rot; c += 32) cs[r * p.rot + c] = p.rope[(base + r) * p.rope_stride + c];
+  }
+  const int page = checked_page(p.batch, id, &g_kv_append_error);
+  __syncthreads();
+  if (page < 0) return;
+  const int off = base % p.batch.page_size;
+
+  // K and V: one head's block per warp
+  for (int task = me; task < tasks; task += workers) {
+    const int which = task >= p.n_kv_heads;
+    const int h = which ? task - p.n_kv_heads : task;
+    uint8_t* codes = p.pages[which] + int64_t(page) * p.page_stride +
+                     (int64_t(h) * p.batch.page_size + off) * D + 8 * l;
+    float* scale = p.scales[which] + int64_t(page) * p.scale_stride + h * (p.batch.page_size / kBlock) + off / kBlock;
     const float old = lo > 0 ? *scale : 0.0f;
+    float x[PASSES][8];
+#pragma unroll
+    for (int i = 0; i < PASSES; ++i) unpack8<T>(raw[i], x[i]);
     if (p.rope && !which) {
 #pragma unroll
       for (int i = 0; i < PASSES; ++i) {
@@ -227,13 +232,15 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     }
     __syncwarp();   // every lane has read the old scale
     if (lane == 0 && sc != old) *scale = sc;
+    if (task + workers < tasks) fetch(task + workers);
   }
 
   // q: rows of (token, head), RPP rows per warp pass
   if (p.q) {
     const int rows = (hi - lo) * p.n_q_heads;
     constexpr int U = 4;
-    for (int r0 = me * RPP * U; r0 < rows; r0 += workers * RPP * U) {
+    // (the last warps first: with few tokens the first ones have a head's keys or values)
+    for (int r0 = (workers - 1 - me) * RPP * U; r0 < rows; r0 += workers * RPP * U) {
       uint4 raw[U];
       int tok[U], head[U];
 #pragma unroll

@@ -112,6 +112,7 @@ struct Shared {
     int cnt, first, last, t0, row0, rows, past, head, dest;
   };
   uint8_t ring[kStages][kStageBytes];
+  uint8_t q[kStages][R * D * 2];               // the item's q rows, in its first stage
   float merge[W][R][kMergeRow];
   float stat[W][R][2];
   Meta meta[kStages];
@@ -151,21 +152,14 @@ __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
   }
 }
 
-// Row tile `row0` of q as the products' column operand: lane (n, t) holds
-// channels [D/4 t, D/4 (t + 1)) of row n. bf16 rows are brought to fp16 over
-// a power of two of their largest magnitude, returned in `factor` (of row n).
+// A row of q as the products' column operand: lane (n, t) holds channels
+// [D/4 t, D/4 (t + 1)) of row n. bf16 rows are brought to fp16 over a power
+// of two of their largest magnitude, returned in `factor` (of row n).
 template <typename T, int D>
-__device__ __forceinline__ void load_q(const AttentionParams& p, int t0, int row, bool there, int head, int t,
-                                       uint32_t (&f)[D / 8], float& factor) {
+__device__ __forceinline__ void load_q(const uint8_t* row, int t, uint32_t (&f)[D / 8], float& factor) {
   uint4 raw[D / 32];
 #pragma unroll
-  for (int i = 0; i < D / 32; ++i) raw[i] = make_uint4(0, 0, 0, 0);
-  if (there) {
-    const uint16_t* src =
-        p.q + int64_t(t0 + row / p.group) * p.q_stride + int64_t(head * p.group + row % p.group) * D + t * (D / 4);
-#pragma unroll
-    for (int i = 0; i < D / 32; ++i) raw[i] = reinterpret_cast<const uint4*>(src)[i];
-  }
+  for (int i = 0; i < D / 32; ++i) raw[i] = *reinterpret_cast<const uint4*>(row + t * (D / 2) + i * 16);
   factor = 1.0f;
   if constexpr (std::is_same<T, __nv_bfloat16>::value) {
     float x[D / 32][8], top = 0.0f;
@@ -343,6 +337,22 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(val ? &m.vs[i] : &m.ks[i])), "l"(sc)
                        : "memory");
         }
+        if (cur.first) {                 // the item's q rows, zeros behind its last
+          constexpr int CPR = D / 8;
+          const uint32_t dst = smem_u32(sh.q[s]);
+#pragma unroll
+          for (int c = lane; c < R * CPR; c += 32) {
+            const int r = c / CPR, row = cur.row0 + r, tok = row / p.group;
+            const bool there = r < cur.rows;
+            const uint16_t* src = p.q;
+            if (there)
+              src += int64_t(cur.t0 + tok) * p.q_stride + int64_t(cur.head * p.group + row - tok * p.group) * D +
+                     (c % CPR) * 8;
+            asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16), "l"(src),
+                         "r"(there ? 16 : 0)
+                         : "memory");
+          }
+        }
         asm volatile("cp.async.mbarrier.arrive.noinc.shared::cta.b64 [%0];" ::"r"(smem_u32(&sh.full[s])) : "memory");
         used |= 1u << s;
         if (++s == kStages) {
@@ -380,7 +390,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mine;
-        load_q<T, D>(p, t0, row0 + nt * 8 + g, nt * 8 + g < rows, head, t, qf[nt], mine);
+        load_q<T, D>(sh.q[s] + (nt * 8 + g) * (D * 2), t, qf[nt], mine);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           factor[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
@@ -585,68 +595,57 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 constexpr int kJoinThreads = 128;
 constexpr int kJoinRows = 4;               // CTAs along y: rows r, r + 4, ...
 
-// Joins the parts of the item that starts in CTA blockIdx.x's run: parts
-// `slot`, then the first part of each CTA up to `last`, in that order.
+// Joins the parts of the item that starts in CTA blockIdx.x's run: part
+// `slot`, then the first part of each CTA up to `last`. A row's parts are
+// taken in turn by GR groups of threads (one pass, with a running maximum, so
+// that all loads go out together), which then meet.
 template <typename T, int D, int R>
-__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionParams p, int grid) {
+__global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constant__ AttentionParams p) {
   constexpr int Q = D / 4;                 // threads along a row
-  constexpr int GR = kJoinThreads / Q;     // parts summed side by side
-  extern __shared__ float weight[];        // [grid]
+  constexpr int GR = kJoinThreads / Q;
   __shared__ float4 sums[GR][Q];
-  __shared__ float red[2][kJoinThreads / 32];
+  __shared__ float2 stats[GR];
   pdl_launch();
   pdl_wait();
   const Join j = p.joins[blockIdx.x];
   if (j.last < 0) return;
   const int c0 = blockIdx.x, n = j.last - c0 + 1;
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
-  const int64_t size = R * (D + 2);
+  const int gr = threadIdx.x / Q, d = threadIdx.x % Q;
   for (int r = blockIdx.y; r < j.rows; r += kJoinRows) {
-    const float* base = p.part;
-    auto part = [&](int i) { return base + int64_t(i == 0 ? j.slot : 2 * (c0 + i)) * size; };
-    float top = -INFINITY;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-      const float v = part(i)[R * D + 2 * r];
-      weight[i] = v;
-      top = fmaxf(top, v);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
-    if (lane == 0) red[0][warp] = top;
-    __syncthreads();
-    top = fmaxf(fmaxf(red[0][0], red[0][1]), fmaxf(red[0][2], red[0][3]));
-    float sum = 0.0f;
-    for (int i = threadIdx.x; i < n; i += kJoinThreads) {
-      const float f = top == -INFINITY ? 0.0f : exp2_fast(weight[i] - top);
-      weight[i] = f;
-      sum = fmaf(f, part(i)[R * D + 2 * r + 1], sum);
-    }
-#pragma unroll
-    for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-    if (lane == 0) red[1][warp] = sum;
-    __syncthreads();
-    sum = (red[1][0] + red[1][1]) + (red[1][2] + red[1][3]);
-    const int gr = threadIdx.x / Q, d = threadIdx.x % Q;
+    float m = -INFINITY, l = 0.0f;
     float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
 #pragma unroll 4
     for (int i = gr; i < n; i += GR) {
-      const float4 x = *reinterpret_cast<const float4*>(part(i) + r * D + 4 * d);
-      const float f = weight[i];
-      o.x = fmaf(f, x.x, o.x);
-      o.y = fmaf(f, x.y, o.y);
-      o.z = fmaf(f, x.z, o.z);
-      o.w = fmaf(f, x.w, o.w);
+      const float* part = p.part + int64_t(i == 0 ? j.slot : 2 * (c0 + i)) * (R * (D + 2));
+      const float2 st = *reinterpret_cast<const float2*>(part + R * D + 2 * r);
+      const float4 x = *reinterpret_cast<const float4*>(part + r * D + 4 * d);
+      const float top = fmaxf(m, st.x), base = top == -INFINITY ? 0.0f : top;
+      const float f = exp2_fast(m - base), g = exp2_fast(st.x - base);
+      m = top;
+      l = fmaf(l, f, g * st.y);
+      o.x = fmaf(o.x, f, g * x.x);
+      o.y = fmaf(o.y, f, g * x.y);
+      o.z = fmaf(o.z, f, g * x.z);
+      o.w = fmaf(o.w, f, g * x.w);
     }
     sums[gr][d] = o;
+    if (d == 0) stats[gr] = make_float2(m, l);
     __syncthreads();
     if (gr == 0) {
+      float top = -INFINITY, sum = 0.0f;
 #pragma unroll
-      for (int i = 1; i < GR; ++i) {
+      for (int i = 0; i < GR; ++i) top = fmaxf(top, stats[i].x);
+      const float base = top == -INFINITY ? 0.0f : top;
+      o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+      for (int i = 0; i < GR; ++i) {
+        const float f = exp2_fast(stats[i].x - base);
         const float4 x = sums[i][d];
-        o.x += x.x;
-        o.y += x.y;
-        o.z += x.z;
-        o.w += x.w;
+        sum = fmaf(f, stats[i].y, sum);
+        o.x = fmaf(f, x.x, o.x);
+        o.y = fmaf(f, x.y, o.y);
+        o.z = fmaf(f, x.z, o.z);
+        o.w = fmaf(f, x.w, o.w);
       }
       const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
       const int row = j.row0 + r;
@@ -665,27 +664,27 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 // host side
 // ---------------------------------------------------------------------------
 using DecodeFn = void (*)(CUtensorMap, CUtensorMap, AttentionParams);
-using JoinFn = void (*)(AttentionParams, int);
-using JoinRowsFn = void (*)(AttentionParams);
+using JoinFn = void (*)(AttentionParams);
 
 // kind 0, 1: up to 8 / 16 rows a tile; 2: pairs of row tiles of 128.
 struct Variant {
   DecodeFn main;
   JoinFn join;
-  JoinRowsFn join_rows;   // kind 2's
   int R, smem, threads;
+  dim3 join_grid;         // y and z of it
+  int join_threads;
 };
 
 template <typename T, int D, int FMT>
 Variant variant_of(int kind) {
   if (kind == 0)
-    return {decode_attention_kernel<T, D, FMT, 1>, join_kernel<T, D, 8>, nullptr, 8, int(sizeof(Shared<D, 8>)) + 1024,
-            kThreads};
+    return {decode_attention_kernel<T, D, FMT, 1>, join_kernel<T, D, 8>, 8, int(sizeof(Shared<D, 8>)) + 1024, kThreads,
+            dim3(1, kJoinRows), kJoinThreads};
   if (kind == 1)
-    return {decode_attention_kernel<T, D, FMT, 2>, join_kernel<T, D, 16>, nullptr, 16,
-            int(sizeof(Shared<D, 16>)) + 1024, kThreads};
-  return {prefill_attention_kernel<T, D, FMT>, nullptr, join_rows_kernel<T, D>, kPairRows,
-          int(sizeof(PreShared<D>)) + 1024, kPreThreads};
+    return {decode_attention_kernel<T, D, FMT, 2>, join_kernel<T, D, 16>, 16, int(sizeof(Shared<D, 16>)) + 1024,
+            kThreads, dim3(1, kJoinRows), kJoinThreads};
+  return {prefill_attention_kernel<T, D, FMT>, join_rows_kernel<T, D>, kPairRows, int(sizeof(PreShared<D>)) + 1024,
+          kPreThreads, dim3(1, kPairRows / 32), 256};
 }
 
 template <typename T>
@@ -743,17 +742,27 @@ awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* 
 
 struct Plan {
   Variant v;
+  bool many;
   int grid;
 };
 
 awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens, int32_t dtype,
                      int32_t n_q_heads, Plan* plan) {
+  const int group = n_q_heads / cache->n_kv_heads;
   const int64_t most = batch->max_q_len > 0 && batch->max_q_len < n_tokens ? batch->max_q_len : n_tokens;
-  const int kind = kind_of(most * (n_q_heads / cache->n_kv_heads));
+  const int kind = kind_of(most * group);
   plan->v = dtype == AWQ_KV_FP16 ? variant_of<__half>(cache->head_dim, cache->format, kind)
                                  : variant_of<__nv_bfloat16>(cache->head_dim, cache->format, kind);
+  plan->many = kind == 2;
   const int key = (((dtype == AWQ_KV_BF16) * 2 + (cache->head_dim == 128)) * 2 + (cache->format == AWQ_KV_E4M3)) * 3 + kind;
-  return resident(plan->v, key, &plan->grid);
+  const awq_status_t st = resident(plan->v, key, &plan->grid);
+  if (st != AWQ_OK) return st;
+  // No more CTAs than the longest sequences that fit could give work to.
+  const int64_t tiles = (int64_t(batch->max_pages) * cache->page_size + kBlock - 1) / kBlock + 1;
+  const int64_t work = plan->many ? (tiles + 7) / 8 * ((n_tokens * group + kPairRows - 1) / kPairRows + batch->n_seqs)
+                                  : (tiles + W - 1) / W * ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs);
+  if (work <= plan->grid / cache->n_kv_heads) plan->grid = int(work > 0 ? work : 1) * cache->n_kv_heads;
+  return AWQ_OK;
 }
 
 }  // namespace
@@ -832,8 +841,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   // A page's tokens of one head are rows of head_dim bytes; a box is one scale block of them.
   CUtensorMap map_k, map_v;
   const uint64_t D = cache->head_dim;
-  const bool many = plan.v.join_rows != nullptr;
-  const CUtensorMapSwizzle sw = many       ? CU_TENSOR_MAP_SWIZZLE_NONE
+  const CUtensorMapSwizzle sw = plan.many  ? CU_TENSOR_MAP_SWIZZLE_NONE
                                 : D == 128 ? CU_TENSOR_MAP_SWIZZLE_128B
                                            : CU_TENSOR_MAP_SWIZZLE_64B;
   // (an empty cache still gets a map: every page id is then out of range and no copy is issued)
@@ -849,12 +857,9 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), plan.v.threads, plan.v.smem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&lc, plan.v.main, map_k, map_v, p);
-  if (e == cudaSuccess && many) {
-    lc = overlapped(dim3(unsigned(plan.grid), kPairRows / 32), 256, 0, stream, &attr);
-    e = cudaLaunchKernelEx(&lc, plan.v.join_rows, p);
-  } else if (e == cudaSuccess) {
-    lc = overlapped(dim3(unsigned(plan.grid), kJoinRows), kJoinThreads, plan.grid * sizeof(float), stream, &attr);
-    e = cudaLaunchKernelEx(&lc, plan.v.join, p, plan.grid);
+  if (e == cudaSuccess) {
+    lc = overlapped(dim3(unsigned(plan.grid), plan.v.join_grid.y), plan.v.join_threads, 0, stream, &attr);
+    e = cudaLaunchKernelEx(&lc, plan.v.join, p);
   }
   if (e != cudaSuccess) {
     cudaGetLastError();
