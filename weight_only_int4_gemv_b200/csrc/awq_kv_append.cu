@@ -19,7 +19,7 @@
 // tokens. Hence one CTA per touched block of 16 tokens (so that a scale and
 // its codes have one writer and no atomics) with the heads spread over
 // blockIdx.y when there are few blocks; the block's table rows are read once
-// into shared memory and used for every head; a warp holds a head's whole
+// into shared memory and used for every head; two warps hold a head's whole
 // block in registers (one read of K and V: the maximum and the codes come
 // from the same values).
 
@@ -57,37 +57,63 @@ __device__ __forceinline__ int touched(const Seq& s) {
   return s.len > p0 ? (s.len - 1) / kBlock - p0 / kBlock + 1 : 0;
 }
 
-// x: channels 8l .. 8l+7 of a row, l the lane's place in the row's lanes.
-// cs: the row's cosines and sines in shared memory.
-template <int LPR>
-__device__ __forceinline__ void rotate8(float (&x)[8], int l, const float* cs, int rot, bool interleaved) {
-  const int half = rot >> 1;
-  const int d0 = 8 * l;
-  if (interleaved) {
-    if (d0 < rot) {
+__device__ __forceinline__ void load4(const float* p, float* v) {
+  const float4 f = *reinterpret_cast<const float4*>(p);
+  v[0] = f.x;
+  v[1] = f.y;
+  v[2] = f.z;
+  v[3] = f.w;
+}
+
+// The rotation of channels 8l .. 8l+7 of a row (l: the lane's place among the
+// row's lanes) by the angles of one position.
+struct Turn {
+  float c[8], s[8];   // interleaved: four of each
+  int src;            // half-width pairs: the lane with the partner channels
+  bool in, interleaved;
+
+  // cs: the position's cosines and sines in shared memory.
+  __device__ __forceinline__ void load(int l, const float* cs, int rot, bool inter) {
+    const int half = rot >> 1, d0 = 8 * l, lane = threadIdx.x & 31;
+    interleaved = inter;
+    in = d0 < rot;
+    src = lane;
+    if (interleaved) {
+      const float* at = cs + (in ? d0 >> 1 : 0);
+      load4(at, c);
+      load4(at + half, s);
+      return;
+    }
+    const bool low = d0 < half;
+    const float* at = cs + (in ? (low ? d0 : d0 - half) : 0);
+    load4(at, c);
+    load4(at + 4, c + 4);
+    load4(at + half, s);
+    load4(at + half + 4, s + 4);
+    if (in) src = low ? lane + (half >> 3) : lane - (half >> 3);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) s[j] = low ? -s[j] : s[j];
+  }
+  // (all lanes of the warp together)
+  __device__ __forceinline__ void apply(float (&x)[8]) const {
+    if (interleaved) {
 #pragma unroll
       for (int j = 0; j < 4; ++j) {
-        const float c = cs[(d0 >> 1) + j], s = cs[half + (d0 >> 1) + j];
         const float a = x[2 * j], b = x[2 * j + 1];
-        x[2 * j] = a * c - b * s;
-        x[2 * j + 1] = b * c + a * s;
+        if (in) {
+          x[2 * j] = a * c[j] - b * s[j];
+          x[2 * j + 1] = b * c[j] + a * s[j];
+        }
       }
+      return;
     }
-    return;
-  }
-  // the partner channels are half a rotation width away, in another lane
-  const bool low = d0 < half, in = d0 < rot;
-  const int lane = threadIdx.x & 31;
-  const int src = in ? (low ? lane + (half >> 3) : lane - (half >> 3)) : lane;
-  float y[8];
 #pragma unroll
-  for (int j = 0; j < 8; ++j) y[j] = __shfl_sync(0xffffffffu, x[j], src);
-  if (in) {
-    const float* c = cs + (low ? d0 : d0 - half);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) x[j] = low ? x[j] * c[j] - y[j] * c[half + j] : x[j] * c[j] + y[j] * c[half + j];
+    for (int j = 0; j < 8; ++j) {
+      const float y = __shfl_sync(0xffffffffu, x[j], src);
+      if (in) x[j] = x[j] * c[j] + y * s[j];
+    }
   }
-}
+};
 
 // x / s (x = hi + lo) rounded to odd in fp32: cut off, with the last bit set
 // where anything was cut, so that rounding it to a code rounds the quotient
@@ -102,39 +128,59 @@ __device__ __forceinline__ float quotient_odd(float hi, float lo, float s, float
   return __uint_as_float(bits);
 }
 
-// Whether t, a quotient within 3 ulp, may lie on the other side of a border
-// between two codes.
-template <int FMT>
-__device__ __forceinline__ bool near_border(float t) {
-  if (FMT == AWQ_KV_INT8) return fabsf(t - rintf(t)) > 0.4999f;   // 127 * 3 * 2^-24 < 10^-4
-  const uint32_t a = __float_as_uint(t) & 0x7fffffffu;
-  // normal codes: the 20 bits that go are near their middle; subnormal ones (below 2^-6): always looked at
-  return ((a - 0x7fff8u) & 0xfffffu) <= 16u || a - 1u < 0x3c7fffffu;
-}
-
-// The codes of eight values over the scale s.
+// The codes of eight values over the scale s (none above it by more than the
+// rounding of top / R). Products by inv give the quotients within 3 ulp; if
+// one of them comes that near to a border between two codes, all eight are
+// settled by their remainders.
 template <int FMT>
 __device__ __forceinline__ uint2 quantize8(const float (&x)[8], float s, float inv) {
-  float t[8];
-  bool near = false;
+  if constexpr (FMT == AWQ_KV_INT8) {
+    // x inv + 1.5 * 2^23 + 128 ends in the rounded integer, offset by 128; |x inv - integer| near 1/2 is a border
+    constexpr float kMagic = 12583040.0f;
+    float y[8], far = 0.0f;
 #pragma unroll
-  for (int j = 0; j < 8; ++j) {
-    t[j] = x[j] * inv;
-    near |= near_border<FMT>(t[j]);
-  }
-  if (near) {
+    for (int j = 0; j < 8; ++j) {
+      y[j] = fmaf(x[j], inv, kMagic);
+      far = fmaxf(far, fabsf(fmaf(x[j], inv, -(y[j] - kMagic))));
+    }
+    if (far > 0.4999f) {   // 127 * 3 * 2^-24 < 10^-4
 #pragma unroll
-    for (int j = 0; j < 8; ++j) t[j] = quotient_odd(x[j], 0.0f, s, inv);
+      for (int j = 0; j < 8; ++j) y[j] = rintf(quotient_odd(x[j], 0.0f, s, inv)) + kMagic;
+    }
+    uint32_t w[2];
+#pragma unroll
+    for (int k = 0; k < 2; ++k) {
+      const uint32_t lo = __byte_perm(__float_as_uint(y[4 * k]), __float_as_uint(y[4 * k + 1]), 0x0040);
+      const uint32_t hi = __byte_perm(__float_as_uint(y[4 * k + 2]), __float_as_uint(y[4 * k + 3]), 0x0040);
+      w[k] = __byte_perm(lo, hi, 0x5410);
+    }
+    return make_uint2(w[0], w[1]);
+  } else {
+    // normal codes: the 20 bits that go are near their middle; subnormal ones (below 2^-6): always looked at
+    float t[8];
+    uint32_t near = 0xffffffffu, least = 0xffffffffu;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+      t[j] = x[j] * inv;
+      const uint32_t b = __float_as_uint(t[j]);
+      near = min(near, (b - 0x7fff8u) & 0xfffffu);
+      least = min(least, (b & 0x7fffffffu) - 1u);
+    }
+    if (near <= 16u || least < 0x3c7fffffu) {
+#pragma unroll
+      for (int j = 0; j < 8; ++j) t[j] = quotient_odd(x[j], 0.0f, s, inv);
+    }
+    return make_uint2(Code<FMT>::encode4(t), Code<FMT>::encode4(t + 4));
   }
-  return make_uint2(Code<FMT>::encode4(t), Code<FMT>::encode4(t + 4));
 }
 
 template <typename T, int D, int FMT>
-__global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant__ AppendParams p) {
+__global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_constant__ AppendParams p) {
   constexpr int LPR = D / 8;            // lanes per row of a head
   constexpr int RPP = 32 / LPR;         // rows per warp pass
-  constexpr int PASSES = kBlock / RPP;
+  constexpr int PASSES = kBlock / 2 / RPP;   // a head's block is two warps' work, eight tokens each
   __shared__ int64_t scratch[40];
+  __shared__ float tops[2][kWarps];
   __shared__ __align__(16) float cs[kBlock * D];
   pdl_launch();
   pdl_wait();
@@ -162,6 +208,7 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5;
   const int l = lane % LPR, sub = lane / LPR;
   const int workers = gridDim.y * kWarps, me = blockIdx.y * kWarps + warp;
+  const int teams = workers / 2, team = me / 2, r_first = (warp & 1) * (kBlock / 2) + sub;
   const int tasks = 2 * p.n_kv_heads;
   uint4 raw[PASSES];
   auto fetch = [&](int task) {                          // K or V rows of one head, zeros around the new ones
@@ -170,11 +217,11 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     const uint16_t* src = (which ? p.v : p.k) + int64_t(t0) * stride + (which ? task - p.n_kv_heads : task) * D + 8 * l;
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int r = i * RPP + sub;
+      const int r = r_first + i * RPP;
       raw[i] = r >= lo && r < hi ? *reinterpret_cast<const uint4*>(src + r * stride) : make_uint4(0, 0, 0, 0);
     }
   };
-  if (me < tasks) fetch(me);
+  if (team < tasks) fetch(team);
   if (p.rope) {
     for (int r = lo + warp; r < hi; r += kWarps)
       for (int c = lane; c < p.rot; c += 32) cs[r * p.rot + c] = p.rope[(base + r) * p.rope_stride + c];
@@ -184,8 +231,8 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
   if (page < 0) return;
   const int off = base % p.batch.page_size;
 
-  // K and V: one head's block per warp
-  for (int task = me; task < tasks; task += workers) {
+  // K and V
+  for (int task = team, round = 0; task < tasks; task += teams, round ^= 1) {
     const int which = task >= p.n_kv_heads;
     const int h = which ? task - p.n_kv_heads : task;
     uint8_t* codes = p.pages[which] + int64_t(page) * p.page_stride +
@@ -193,27 +240,31 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
     float* scale = p.scales[which] + int64_t(page) * p.scale_stride + h * (p.batch.page_size / kBlock) + off / kBlock;
     const float old = lo > 0 ? *scale : 0.0f;
     float x[PASSES][8];
-#pragma unroll
-    for (int i = 0; i < PASSES; ++i) unpack8<T>(raw[i], x[i]);
-    if (p.rope && !which) {
-#pragma unroll
-      for (int i = 0; i < PASSES; ++i) {
-        const int r = min(max(i * RPP + sub, lo), hi - 1);   // other rows hold zeros, which turn to zeros
-        rotate8<LPR>(x[i], l, cs + r * p.rot, p.rot, p.interleaved);
-      }
-    }
     float top = 0.0f;
 #pragma unroll
-    for (int i = 0; i < PASSES; ++i)
+    for (int i = 0; i < PASSES; ++i) {
+      unpack8<T>(raw[i], x[i]);
+      const int r = min(max(r_first + i * RPP, lo), hi - 1);   // other rows hold zeros, which turn to zeros
+      if (p.rope && !which) {
+        Turn turn;
+        turn.load(l, cs + r * p.rot, p.rot, p.interleaved);
+        turn.apply(x[i]);
+      }
 #pragma unroll
       for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i][j]));
+    }
+    if (task + teams < tasks) fetch(task + teams);
 #pragma unroll
     for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    if (lane == 0) tops[round][warp] = top;
+    // (both warps have read the old scale, too)
+    asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
+    top = fmaxf(top, tops[round][warp ^ 1]);
     const float sc = fmaxf(fmaxf(__fdiv_rn(top, Code<FMT>::kTop), old), kScaleFloor);
     const float inv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {
-      const int r = i * RPP + sub;
+      const int r = r_first + i * RPP;
       uint2* dst = reinterpret_cast<uint2*>(codes + r * D);
       if (r >= lo && r < hi) {
         *dst = quantize8<FMT>(x[i], sc, inv);
@@ -230,38 +281,40 @@ __global__ void __launch_bounds__(kThreads) append_kernel(const __grid_constant_
         *dst = make_uint2(Code<FMT>::encode4(t), Code<FMT>::encode4(t + 4));
       }
     }
-    __syncwarp();   // every lane has read the old scale
-    if (lane == 0 && sc != old) *scale = sc;
-    if (task + workers < tasks) fetch(task + workers);
+    if (lane == 0 && !(warp & 1) && sc != old) *scale = sc;
   }
 
-  // q: rows of (token, head), RPP rows per warp pass
+  // q: a warp takes U * RPP heads of a token, whose angles it loads once
   if (p.q) {
-    const int rows = (hi - lo) * p.n_q_heads;
     constexpr int U = 4;
+    const int per_token = (p.n_q_heads + U * RPP - 1) / (U * RPP);
     // (the last warps first: with few tokens the first ones have a head's keys or values)
-    for (int r0 = (workers - 1 - me) * RPP * U; r0 < rows; r0 += workers * RPP * U) {
+    for (int u = workers - 1 - me; u < (hi - lo) * per_token; u += workers) {
+      const int i = u / per_token, h0 = (u - i * per_token) * (U * RPP) + sub;
+      const int64_t row = t0 + lo + i;
+      const uint16_t* src = p.q + row * p.q_stride + 8 * l;
+      uint16_t* dst = p.q_out + row * p.q_out_stride + 8 * l;
       uint4 raw[U];
-      int tok[U], head[U];
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        const int r = r0 + u * RPP + sub;
-        raw[u] = make_uint4(0, 0, 0, 0);
-        tok[u] = r < rows ? lo + r / p.n_q_heads : -1;
-        head[u] = r % p.n_q_heads;
-        if (tok[u] >= 0)
-          raw[u] = *reinterpret_cast<const uint4*>(p.q + int64_t(t0 + tok[u]) * p.q_stride + head[u] * D + 8 * l);
+      for (int k = 0; k < U; ++k) {
+        const int h = h0 + k * RPP;
+        raw[k] = h < p.n_q_heads ? *reinterpret_cast<const uint4*>(src + h * D) : make_uint4(0, 0, 0, 0);
+      }
+      if (p.rope) {
+        Turn turn;
+        turn.load(l, cs + (lo + i) * p.rot, p.rot, p.interleaved);
+#pragma unroll
+        for (int k = 0; k < U; ++k) {
+          float x[8];
+          unpack8<T>(raw[k], x);
+          turn.apply(x);
+          raw[k] = pack8<T>(x);
+        }
       }
 #pragma unroll
-      for (int u = 0; u < U; ++u) {
-        if (p.rope) {
-          float x[8];
-          unpack8<T>(raw[u], x);
-          rotate8<LPR>(x, l, cs + max(tok[u], lo) * p.rot, p.rot, p.interleaved);
-          raw[u] = pack8<T>(x);
-        }
-        if (tok[u] >= 0)
-          *reinterpret_cast<uint4*>(p.q_out + int64_t(t0 + tok[u]) * p.q_out_stride + head[u] * D + 8 * l) = raw[u];
+      for (int k = 0; k < U; ++k) {
+        const int h = h0 + k * RPP;
+        if (h < p.n_q_heads) *reinterpret_cast<uint4*>(dst + h * D) = raw[k];
       }
     }
   }
@@ -315,10 +368,11 @@ __global__ void __launch_bounds__(kThreads) dequant_kv_kernel(const __grid_const
   }
 }
 
-// CTAs along y for `blocks` blocks of `work` warp tasks each: enough that a
-// few tokens still use many SMs, no more than there are tasks.
+// CTAs along y for `blocks` blocks of `tasks` warp tasks each: one to two
+// waves of CTAs, so that neither a few tokens nor a wave's remainder leave SMs idle,
+// and no more than there are tasks.
 int spread(int64_t blocks, int64_t tasks, int sms) {
-  const int64_t want = (2 * sms + blocks - 1) / blocks, most = (tasks + kWarps - 1) / kWarps;
+  const int64_t want = (4 * sms + blocks - 1) / blocks, most = (tasks + kWarps - 1) / kWarps;
   return int(want < 1 ? 1 : want > most ? most : want);
 }
 
@@ -435,10 +489,9 @@ extern "C" awq_status_t awq_kv_append(const awq_kv_cache_t* cache, const awq_kv_
   int sms = 0;
   if ((st = sm_count(&sms)) != AWQ_OK) return st;
   const int64_t blocks = slots(n_tokens, batch->n_seqs);
-  // warp tasks of a block: a head's K or V, or a pass of q rows
-  const int64_t per_pass = 4 * 32 / (cache->head_dim / 8);
-  const int64_t rows = int64_t(p.n_q_heads) * (n_tokens < kBlock ? n_tokens : kBlock);
-  const int y = spread(blocks, 2 * cache->n_kv_heads + (rows + per_pass - 1) / per_pass, sms);
+  // warp tasks of a block: two for a head's keys and two for its values, one for some heads of a token's q
+  const int64_t heads = 4 * 32 / (cache->head_dim / 8), per_token = (p.n_q_heads + heads - 1) / heads;
+  const int y = spread(blocks, 4 * cache->n_kv_heads + per_token * (n_tokens < kBlock ? n_tokens : kBlock), sms);
   return launch(dtype == AWQ_KV_FP16 ? append_fn<__half>(cache->head_dim, cache->format)
                                      : append_fn<__nv_bfloat16>(cache->head_dim, cache->format),
                 dim3(unsigned(blocks), unsigned(y)), p, stream);
