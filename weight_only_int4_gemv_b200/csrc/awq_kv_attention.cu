@@ -52,6 +52,7 @@ __device__ uint32_t g_kv_attention_error = 0;
 constexpr int W = 4;                       // consumer warps
 constexpr int kThreads = (W + 1) * 32;
 constexpr int kStages = 3;
+constexpr int kItems = 8;                  // more than the stages in the ring and the one ahead of it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
 
@@ -109,17 +110,47 @@ struct Shared {
   struct Meta {
     int tile[W];            // position of the tile's first key, -1: nothing there
     float ks[W], vs[W];
-    int cnt, first, last, t0, row0, rows, past, head, dest;
+    int flags;
+  };
+  struct Item {
+    int t0, row0, rows, past, head, dest;
   };
   uint8_t ring[kStages][kStageBytes];
   uint8_t q[kStages][R * D * 2];               // the item's q rows, in its first stage
   float merge[W][R][kMergeRow];
   float stat[W][R][2];
   Meta meta[kStages];
+  Item items[kItems];
   uint64_t full[kStages], empty[kStages], merged, taken;
   int64_t scratch[40];
   int abort;
 };
+
+constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
+
+// A bounded wait in few instructions: it is inlined in many places, and a
+// warp that polls shares its scheduler with one that works.
+__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+  for (long long t0 = 0;;) {
+    uint32_t ok;
+    asm volatile(
+        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+        "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+        "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t@q bra POLL_%=;\n"
+        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+        : "=r"(ok)
+        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+        : "memory");
+    if (ok) return true;
+    const long long t = clock64();
+    if (t0 == 0) t0 = t;
+    if (t - t0 > kWaitCycles || *abort) {
+      *abort = 1;
+      atomicOr(err, kErrWait);
+      return false;
+    }
+  }
+}
 
 __device__ __forceinline__ void mma_16816(float (&c)[4], const uint32_t (&a)[4], uint32_t b0, uint32_t b1) {
   asm volatile(
@@ -140,16 +171,32 @@ __device__ __forceinline__ float exp2_fast(float x) {
   return r;
 }
 
-// Two codes (bytes LO, LO + 1 of w) as an fp16 pair, exactly. int8: a byte u
-// under 0x64 is the fp16 number 1024 + u = 1152 + code.
+// Codes as fp16, exactly but for a power of two (kShift). int8: a byte u under
+// 0x64 is the fp16 number 1024 + u = 1152 + code. e4m3: exponent and mantissa
+// in the places of fp16's are the number times 2^-8 (the exponents' biases are
+// 7 and 15; subnormal numbers too), in half the instructions of a conversion
+// by cvt. (The NaN codes, which the cache never gets, come out as 480.)
+template <int FMT>
+constexpr float kShift = FMT == AWQ_KV_E4M3 ? 256.0f : 1.0f;
+
+// Bytes 0 and 2 of w.
+template <int FMT>
+__device__ __forceinline__ uint32_t code_even(uint32_t w) {
+  if constexpr (FMT == AWQ_KV_INT8) return hsub2_u32(lop3_and_or(w, 0x00ff00ffu, 0x64006400u), 0x64806480u);
+  return (w & 0x007f007fu) * 128u + (w & 0x00800080u) * 256u;
+}
+// Bytes 1 and 3 of w.
+template <int FMT>
+__device__ __forceinline__ uint32_t code_odd(uint32_t w) {
+  if constexpr (FMT == AWQ_KV_INT8) return hsub2_u32(__byte_perm(w, 0x64646464u, 0x4341), 0x64806480u);
+  return ((w & 0x7f007f00u) >> 1) | (w & 0x80008000u);
+}
+// Bytes LO and LO + 1 of w.
 template <int FMT, int LO>
 __device__ __forceinline__ uint32_t code_pair(uint32_t w) {
-  if constexpr (FMT == AWQ_KV_INT8) {
-    return hsub2_u32(__byte_perm(w, 0x64646464u, LO ? 0x4342 : 0x4140), 0x64806480u);
-  } else {
-    const __half2_raw r = __nv_cvt_fp8x2_to_halfraw2(__nv_fp8x2_storage_t(LO ? w >> 16 : w & 0xffffu), __NV_E4M3);
-    return uint32_t(r.x) | (uint32_t(r.y) << 16);
-  }
+  if constexpr (FMT == AWQ_KV_INT8) return hsub2_u32(__byte_perm(w, 0x64646464u, LO ? 0x4342 : 0x4140), 0x64806480u);
+  const uint32_t z = __byte_perm(w, 0u, LO ? 0x4342 : 0x4140) * 128u;
+  return z + (z & 0x40004000u);
 }
 
 // A row of q as the products' column operand: lane (n, t) holds channels
@@ -184,10 +231,11 @@ __device__ __forceinline__ void load_q(const uint8_t* row, int t, uint32_t (&f)[
   }
 #pragma unroll
   for (int i = 0; i < D / 32; ++i) {
-    f[4 * i] = raw[i].x;
-    f[4 * i + 1] = raw[i].y;
-    f[4 * i + 2] = raw[i].z;
-    f[4 * i + 3] = raw[i].w;
+    // channels (0, 2), (1, 3) of each four, as code_even and code_odd give them
+    f[4 * i] = __byte_perm(raw[i].x, raw[i].y, 0x5410);
+    f[4 * i + 1] = __byte_perm(raw[i].x, raw[i].y, 0x7632);
+    f[4 * i + 2] = __byte_perm(raw[i].z, raw[i].w, 0x5410);
+    f[4 * i + 3] = __byte_perm(raw[i].z, raw[i].w, 0x7632);
   }
 }
 
@@ -218,7 +266,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   pdl_wait();
   // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_sleep(bar, parity, abort, err, kErrWait)) != 0;
+    return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
   };
 
   // this CTA's run of units
@@ -248,61 +296,73 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       int b = b_first;
       Seq seq = load_seq(p.batch, b, err);
       Span a = span_of<R>(p, seq);
-      int item = int(rest / a.tiles), tile = int(rest % a.tiles);
-      int64_t u = u0;
-      // one stage: up to W tiles of one item; lane i < W holds tile i's key copy, lane W + i its value copy
+      int item = int(rest / a.tiles), tile = int(rest % a.tiles), items = a.row_tiles * p.n_kv_heads, left = int(u1 - u0);
+      const int32_t* table = p.batch.table + int64_t(b) * p.batch.table_stride;
+      uint32_t n_items = 0;
+      bool fresh = true;             // the next stage begins an item, or this run
+      const int i = lane % W;
+      // One stage ahead of the copies: the tiles of the next stage, and the loads of its pages' ids. lane i < W: tile
+      // i's keys, lane W + i: its values. What an item's stages share goes to a ring of its own.
       struct Stage {
-        int cnt, first, last, t0, row0, rows, past, head, dest, pos, id;
+        int flags, pos, id;          // flags: first | last << 1 | count << 2 | item's place << 8
       };
       auto next = [&](Stage& st) {
-        while (item >= a.row_tiles * p.n_kv_heads) {   // on to the next sequence with rows
-          seq = load_seq(p.batch, ++b, err);
-          a = span_of<R>(p, seq);
-          item = 0;
+        if (fresh) {
+          while (item >= items) {    // on to the next sequence with rows
+            seq = load_seq(p.batch, ++b, err);
+            a = span_of<R>(p, seq);
+            item = 0;
+            items = a.row_tiles * p.n_kv_heads;
+            table = p.batch.table + int64_t(b) * p.batch.table_stride;
+          }
+          const int row_tile = item / p.n_kv_heads;
+          const int64_t begin = u1 - left - tile, end = begin + a.tiles;
+          const int dest = begin >= u0 && end <= u1 ? -1 : int(2 * blockIdx.x) + (begin > u0);
+          ++n_items;
+          auto& it = sh.items[n_items % kItems];
+          const int row0 = row_tile * R, rows = min(R, seq.n * p.group - row0), head = item - row_tile * p.n_kv_heads;
+          if (lane == 0) {
+            it.t0 = seq.t0;
+            it.row0 = row0;
+            it.rows = rows;
+            it.past = seq.past;
+            it.head = head;
+            it.dest = dest;
+          }
+          if (begin >= u0 && end > u1) {
+            join.last = int((end - 1) / per);
+            join.slot = dest;
+            join.t0 = seq.t0;
+            join.row0 = row0;
+            join.rows = rows;
+            join.head = head;
+          }
         }
-        const int left = int(min(int64_t(a.tiles - tile), u1 - u));
-        st.cnt = min(W, left);
-        const int64_t begin = u - tile, end = begin + a.tiles;
-        st.first = u == u0 || tile == 0;
-        st.last = st.cnt == left;
-        st.head = item % p.n_kv_heads;
-        st.row0 = item / p.n_kv_heads * R;
-        st.rows = min(R, seq.n * p.group - st.row0);
-        st.t0 = seq.t0;
-        st.past = seq.past;
-        const bool whole = begin >= u0 && end <= u1;
-        st.dest = whole ? -1 : int(2 * blockIdx.x) + (begin > u0);
-        if (begin >= u0 && end > u1) {
-          join.last = int((end - 1) / per);
-          join.slot = st.dest;
-          join.t0 = st.t0;
-          join.row0 = st.row0;
-          join.rows = st.rows;
-          join.head = st.head;
-        }
-        const int i = lane % W, v = tile + i;
+        const int rem = min(a.tiles - tile, left), cnt = min(W, rem), v = tile + i;
+        st.flags = int(fresh) | (rem <= W ? 2 : 0) | cnt << 2 | int(n_items % kItems) << 8;
         st.pos = -1;
         st.id = -1;
-        if (lane < 2 * W && i < st.cnt) {
+        if (lane < 2 * W && i < cnt) {
           const int pos = (v < a.sink_tiles ? v : v - a.sink_tiles + a.w0) * kBlock;
           if (pos < seq.len) {
             st.pos = pos;
-            st.id = p.batch.table[int64_t(b) * p.batch.table_stride + pos / p.batch.page_size];
+            st.id = table[pos / p.batch.page_size];
           }
         }
-        u += st.cnt;
-        tile += st.cnt;
-        if (tile == a.tiles) {
+        left -= cnt;
+        tile += cnt;
+        fresh = tile == a.tiles;
+        if (fresh) {
           tile = 0;
           ++item;
         }
       };
       Stage cur, after;
-      bool more = u < u1;
+      bool more = left > 0;
       if (more) next(cur);
       while (more) {
-        more = u < u1;
-        if (more) next(after);         // its page ids load while the current stage is issued
+        more = left > 0;
+        if (more) next(after);
         if (!wait(&sh.empty[s], ph ^ 1)) {
           ok = false;
           break;
@@ -310,44 +370,34 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         int page = -1;
         if (cur.pos >= 0) page = checked_page(p.batch, cur.id, err);
         auto& m = sh.meta[s];
-        const int i = lane % W;
         const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
         if (lane < W) m.tile[i] = page >= 0 ? cur.pos : -1;
-        if (lane == 0) {
-          m.cnt = cur.cnt;
-          m.first = cur.first;
-          m.last = cur.last;
-          m.t0 = cur.t0;
-          m.row0 = cur.row0;
-          m.rows = cur.rows;
-          m.past = cur.past;
-          m.head = cur.head;
-          m.dest = cur.dest;
-        }
+        if (lane == 0) m.flags = cur.flags;
         __syncwarp();   // the lanes' entries, before the arrival that publishes them
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(__popc(here)) * Sh::kTile);
         __syncwarp();
+        const auto& it = sh.items[cur.flags >> 8];
         if (page >= 0) {
           const bool val = lane >= W;
-          const int off = cur.pos % p.batch.page_size;
-          tma_load_4d(&sh.ring[s][(val ? W * Sh::kTile : 0) + i * Sh::kTile], val ? &map_v : &map_k, 0, off, cur.head,
-                      page, &sh.full[s]);
+          const int off = cur.pos % p.batch.page_size, head = it.head;
+          tma_load_4d(&sh.ring[s][(val ? W * Sh::kTile : 0) + i * Sh::kTile], val ? &map_v : &map_k, 0, off, head, page,
+                      &sh.full[s]);
           const float* sc = (val ? p.v_scales : p.k_scales) + int64_t(page) * p.scale_stride +
-                            cur.head * (p.batch.page_size / kBlock) + off / kBlock;
+                            head * (p.batch.page_size / kBlock) + off / kBlock;
           asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(smem_u32(val ? &m.vs[i] : &m.ks[i])), "l"(sc)
                        : "memory");
         }
-        if (cur.first) {                 // the item's q rows, zeros behind its last
+        if (cur.flags & 1) {             // the item's q rows, zeros behind its last
           constexpr int CPR = D / 8;
           const uint32_t dst = smem_u32(sh.q[s]);
+          const int t0 = it.t0, row0 = it.row0, rows = it.rows, head = it.head;
 #pragma unroll
           for (int c = lane; c < R * CPR; c += 32) {
-            const int r = c / CPR, row = cur.row0 + r, tok = row / p.group;
-            const bool there = r < cur.rows;
+            const int r = c / CPR, row = row0 + r, tok = row / p.group;
+            const bool there = r < rows;
             const uint16_t* src = p.q;
             if (there)
-              src += int64_t(cur.t0 + tok) * p.q_stride + int64_t(cur.head * p.group + row - tok * p.group) * D +
-                     (c % CPR) * 8;
+              src += int64_t(t0 + tok) * p.q_stride + int64_t(head * p.group + row - tok * p.group) * D + (c % CPR) * 8;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16), "l"(src),
                          "r"(there ? 16 : 0)
                          : "memory");
@@ -365,8 +415,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     if (lane == 0) p.joins[blockIdx.x] = join;
     if (!ok) {
       // every copy issued lands before the CTA's shared memory goes
-      for (int i = 0; i < kStages; ++i)
-        if (used & (1u << i)) wait_sleep_teardown(&sh.full[i], i < s ? ph : ph ^ 1);
+      for (int k = 0; k < kStages; ++k)
+        if (used & (1u << k)) wait_sleep_teardown(&sh.full[k], k < s ? ph : ph ^ 1);
     }
     return;
   }
@@ -378,22 +428,29 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   int at[NT][2];                     // positions of those rows
   float m[NT][2], l[NT][2];
   float acc[NT][D / 16][4];
-  int p_low = 0, p_high = 0;
+  int p_low = 0, p_high = 0;         // the lowest and highest of them
+  int t0 = 0, row0 = 0, rows = 0, head = 0, dest = 0;
   int s = 0;
   uint32_t ph = 0, merges = 0;
   for (int64_t u = u0; u < u1;) {
     if (!wait(&sh.full[s], ph)) return;
     const auto& me = sh.meta[s];
-    const int first = me.first, last = me.last, t0 = me.t0, row0 = me.row0, rows = me.rows, past = me.past,
-              head = me.head, dest = me.dest, cnt = me.cnt, tile = me.tile[warp];
-    if (first) {
+    const int flags = me.flags, tile = me.tile[warp];
+    if (flags & 1) {
+      const auto& it = sh.items[flags >> 8];
+      t0 = it.t0;
+      row0 = it.row0;
+      rows = it.rows;
+      head = it.head;
+      dest = it.dest;
+      const int past = it.past;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mine;
         load_q<T, D>(sh.q[s] + (nt * 8 + g) * (D * 2), t, qf[nt], mine);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          factor[nt][e] = p.scale_log2 * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
+          factor[nt][e] = p.scale_log2 * kShift<FMT> * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
           at[nt][e] = past + (row0 + nt * 8 + 2 * t + e) / p.group;
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.0f;
@@ -429,14 +486,14 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
         for (int w = 0; w < 4; ++w) {
-          const uint32_t a[4] = {code_pair<FMT, 0>(wl[w]), code_pair<FMT, 0>(wh[w]), code_pair<FMT, 2>(wl[w]),
-                                 code_pair<FMT, 2>(wh[w])};
+          const uint32_t a[4] = {code_even<FMT>(wl[w]), code_even<FMT>(wh[w]), code_odd<FMT>(wl[w]),
+                                 code_odd<FMT>(wh[w])};
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[nt][8 * i + 2 * w], qf[nt][8 * i + 2 * w + 1]);
         }
       }
       // weights
-      const float lv = __log2f(vs), iv = __fdividef(1.0f, vs);
+      const float lv = __log2f(vs), iv = __fdividef(1.0f / kShift<FMT>, vs);   // (O holds codes / kShift)
       const bool all = tile + kBlock - 1 <= p_low &&
                        (p.window == 0 || tile > p_high - p.window || tile + kBlock <= p.sinks);
       bool raise = false;
@@ -501,20 +558,14 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
           vw[i][0] = x.x;
           vw[i][1] = x.y;
         }
-        // e4m3 bytes behind the sequence's end may be NaN, which a weight of 0 does not silence
-        if (FMT == AWQ_KV_E4M3 && !all && tile + r > p_high) {
-#pragma unroll
-          for (int w = 0; w < D / 32; ++w) vw[i][w] = 0;
-        }
       }
 #pragma unroll
       for (int w = 0; w < D / 32; ++w) {
-        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5140), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7362);
-        const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5140), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7362);
-        const uint32_t a0[4] = {code_pair<FMT, 0>(x0), code_pair<FMT, 2>(x0), code_pair<FMT, 0>(x1),
-                                code_pair<FMT, 2>(x1)};
-        const uint32_t a1[4] = {code_pair<FMT, 0>(y0), code_pair<FMT, 2>(y0), code_pair<FMT, 0>(y1),
-                                code_pair<FMT, 2>(y1)};
+        // two channels of two keys to a word
+        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+        const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+        const uint32_t a0[4] = {code_even<FMT>(x0), code_odd<FMT>(x0), code_even<FMT>(x1), code_odd<FMT>(x1)};
+        const uint32_t a1[4] = {code_even<FMT>(y0), code_odd<FMT>(y0), code_even<FMT>(y1), code_odd<FMT>(y1)};
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt) {
           mma_16816(acc[nt][2 * w], a0, b0[nt], b1[nt]);
@@ -524,12 +575,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[s]);
-    u += cnt;
+    u += (flags >> 2) & 63;
     if (++s == kStages) {
       s = 0;
       ph ^= 1;
     }
-    if (!last) continue;
+    if (!(flags & 2)) continue;
 
     // join the warps' parts of the item
     if (merges && !wait(&sh.taken, (merges - 1) & 1)) return;

@@ -39,7 +39,6 @@ constexpr int kPreThreads = (kSoftmaxWarps + kWidenWarps + 4) * 32;
 // that much longer.
 constexpr int kSegmentCost = 2;
 constexpr float kLeastA = 7.888609052210118e-31f;    // 2^-100
-constexpr long long kWaitCycles = 4000000000ll;  // about 2 s
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
 enum : int {                                   // PreMeta::flags
@@ -52,9 +51,8 @@ enum : int {                                   // PreMeta::flags
 };
 
 struct PreMeta {
-  int pos, valid, flags;
+  int pos, flags;
   int t0, row0, rows, past, head, dest;
-  int pad[3];
   float ks[8], vs[8];            // the blocks' scales
   float a[8], lv[8], iv[8];      // scale log2(e) s_k, log2(s_v), 1 / s_v
 };
@@ -261,30 +259,6 @@ __device__ __forceinline__ float extreme16(const uint32_t* r, Op3 op) {
   auto f = [&](int i) { return __uint_as_float(r[i]); };
   const float a = op(f(0), f(1), f(2)), b = op(f(3), f(4), f(5)), c = op(f(6), f(7), f(8)), d = op(f(9), f(10), f(11));
   return op(op(a, b, f(12)), op(c, d, f(13)), op(f(14), f(15), f(15)));
-}
-
-// A bounded wait in few instructions: it is inlined in many places, and a
-// warp that polls shares its scheduler with one that works.
-__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
-  for (long long t0 = 0;;) {
-    uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-        "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t@q bra POLL_%=;\n"
-        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
-    if (ok) return true;
-    const long long t = clock64();
-    if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitCycles || *abort) {
-      *abort = 1;
-      atomicOr(err, kErrWait);
-      return false;
-    }
-  }
 }
 
 template <typename T, int D, int FMT>
@@ -557,14 +531,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const int mi = it % kMetaSlots;
       if (!wait(&sh.meta_full[mi], (it / kMetaSlots) & 1)) break;
       const PreMeta& me = sh.meta[mi];
-      const int flags = me.flags, valid = me.valid;
+      const int flags = me.flags;
       if (flags & kStop) break;
       if (tid < 8) {                             // (published with the keys)
         PreMeta& out = sh.meta[mi];
-        const float a = fmaxf(fabsf(p.scale_log2) * me.ks[tid], kLeastA);
+        const float a = fmaxf(fabsf(p.scale_log2) * kShift<FMT> * me.ks[tid], kLeastA);
         out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
         out.lv[tid] = __log2f(me.vs[tid]);
-        out.iv[tid] = __fdividef(1.0f, me.vs[tid]);
+        out.iv[tid] = __fdividef(1.0f / kShift<FMT>, me.vs[tid]);   // (O holds codes / kShift)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
@@ -581,9 +555,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         uint8_t* half = sh.half[hs] + half_at;
 #pragma unroll 4
         for (int i = 0; i < kTile / kRowStep; ++i) {
-          uint4 w = *reinterpret_cast<const uint4*>(raw + i * kRowStep * D);
-          // e4m3 bytes behind the end may be NaN, which a weight of 0 does not silence
-          if (FMT == AWQ_KV_E4M3 && r0 + i * kRowStep >= valid) w = make_uint4(0, 0, 0, 0);
+          const uint4 w = *reinterpret_cast<const uint4*>(raw + i * kRowStep * D);
           uint4 a, b;
           widen16<FMT>(w, a, b);
           *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c0) = a;
@@ -730,7 +702,6 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
                            : "memory");
               if (lane == 0) {
                 me.pos = pos;
-                me.valid = min(kTile, s.len - pos);
                 me.flags = flags;
                 me.t0 = s.t0;
                 me.row0 = pr * kPairRows;
