@@ -51,7 +51,9 @@ __device__ uint32_t g_kv_attention_error = 0;
 
 constexpr int W = 4;                       // consumer warps
 constexpr int kThreads = (W + 1) * 32;
-constexpr int kStages = 3;
+constexpr int U = 2;                       // tiles of a warp in a stage
+constexpr int WT = W * U;                  // tiles of a stage
+constexpr int kStages = 2;
 constexpr int kItems = 8;                  // more than the stages in the ring and the one ahead of it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
@@ -105,11 +107,11 @@ __device__ __forceinline__ Span span_of(const AttentionParams& p, const Seq& s) 
 template <int D, int R>
 struct Shared {
   static constexpr int kTile = kBlock * D;              // bytes of 16 keys or values
-  static constexpr int kStageBytes = 2 * W * kTile;
+  static constexpr int kStageBytes = 2 * WT * kTile;
   static constexpr int kMergeRow = D + 4;
   struct Meta {
-    int tile[W];            // position of the tile's first key, -1: nothing there
-    float ks[W], vs[W];
+    int tile[WT];           // position of the tile's first key, -1: nothing there
+    float ks[WT], vs[WT];
     int flags;
   };
   struct Item {
@@ -240,7 +242,7 @@ __device__ __forceinline__ void load_q(const uint8_t* row, int t, uint32_t (&f)[
 }
 
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, NT == 1 ? 3 : 2)
+__global__ void __launch_bounds__(kThreads, 2)
 decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ AttentionParams p) {
   constexpr int R = 8 * NT;
@@ -279,7 +281,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       },
       [&](int64_t sum) {
         per = (sum + gridDim.x - 1) / gridDim.x;
-        per = (per + W - 1) / W * W;
+        per = (per + WT - 1) / WT * WT;
         return per * blockIdx.x;
       },
       &rest, &total);
@@ -300,9 +302,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       const int32_t* table = p.batch.table + int64_t(b) * p.batch.table_stride;
       uint32_t n_items = 0;
       bool fresh = true;             // the next stage begins an item, or this run
-      const int i = lane % W;
-      // One stage ahead of the copies: the tiles of the next stage, and the loads of its pages' ids. lane i < W: tile
-      // i's keys, lane W + i: its values. What an item's stages share goes to a ring of its own.
+      const int i = lane % WT;
+      // One stage ahead of the copies: the tiles of the next stage, and the loads of its pages' ids. lane i < WT: tile
+      // i's keys, lane WT + i: its values. What an item's stages share goes to a ring of its own.
       struct Stage {
         int flags, pos, id;          // flags: first | last << 1 | count << 2 | item's place << 8
       };
@@ -338,11 +340,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             join.head = head;
           }
         }
-        const int rem = min(a.tiles - tile, left), cnt = min(W, rem), v = tile + i;
-        st.flags = int(fresh) | (rem <= W ? 2 : 0) | cnt << 2 | int(n_items % kItems) << 8;
+        const int rem = min(a.tiles - tile, left), cnt = min(WT, rem), v = tile + i;
+        st.flags = int(fresh) | (rem <= WT ? 2 : 0) | cnt << 2 | int(n_items % kItems) << 8;
         st.pos = -1;
         st.id = -1;
-        if (lane < 2 * W && i < cnt) {
+        if (lane < 2 * WT && i < cnt) {
           const int pos = (v < a.sink_tiles ? v : v - a.sink_tiles + a.w0) * kBlock;
           if (pos < seq.len) {
             st.pos = pos;
@@ -371,16 +373,16 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         if (cur.pos >= 0) page = checked_page(p.batch, cur.id, err);
         auto& m = sh.meta[s];
         const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
-        if (lane < W) m.tile[i] = page >= 0 ? cur.pos : -1;
+        if (lane < WT) m.tile[i] = page >= 0 ? cur.pos : -1;
         if (lane == 0) m.flags = cur.flags;
         __syncwarp();   // the lanes' entries, before the arrival that publishes them
         if (lane == 0) mbar_arrive_expect_tx(&sh.full[s], uint32_t(__popc(here)) * Sh::kTile);
         __syncwarp();
         const auto& it = sh.items[cur.flags >> 8];
         if (page >= 0) {
-          const bool val = lane >= W;
+          const bool val = lane >= WT;
           const int off = cur.pos % p.batch.page_size, head = it.head;
-          tma_load_4d(&sh.ring[s][(val ? W * Sh::kTile : 0) + i * Sh::kTile], val ? &map_v : &map_k, 0, off, head, page,
+          tma_load_4d(&sh.ring[s][(val ? WT * Sh::kTile : 0) + i * Sh::kTile], val ? &map_v : &map_k, 0, off, head, page,
                       &sh.full[s]);
           const float* sc = (val ? p.v_scales : p.k_scales) + int64_t(page) * p.scale_stride +
                             head * (p.batch.page_size / kBlock) + off / kBlock;
@@ -435,7 +437,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   for (int64_t u = u0; u < u1;) {
     if (!wait(&sh.full[s], ph)) return;
     const auto& me = sh.meta[s];
-    const int flags = me.flags, tile = me.tile[warp];
+    const int flags = me.flags;
     if (flags & 1) {
       const auto& it = sh.items[flags >> 8];
       t0 = it.t0;
@@ -463,62 +465,82 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       p_low = past + row0 / p.group;
       p_high = past + (row0 + rows - 1) / p.group;
     }
-    if (tile >= 0) {
-      const uint8_t* kt = &sh.ring[s][warp * Sh::kTile];
-      const uint8_t* vt = &sh.ring[s][(W + warp) * Sh::kTile];
-      const float ks = me.ks[warp], vs = me.vs[warp];
-      // S = K q^T
-      float sc[NT][4];
+    // N tiles of the warp together, W apart: their loads, products and exponentials overlap
+    auto take = [&](auto count, int first) {
+      constexpr int N = decltype(count)::value;
+      const uint8_t* kt[N];
+      const uint8_t* vt[N];
+      int tile[N];
+      float ks[N], lv[N], iv[N];
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt) sc[nt][0] = sc[nt][1] = sc[nt][2] = sc[nt][3] = 0.0f;
+      for (int u = 0; u < N; ++u) {
+        const int i = first + u * W;
+        kt[u] = &sh.ring[s][i * Sh::kTile];
+        vt[u] = &sh.ring[s][(WT + i) * Sh::kTile];
+        tile[u] = me.tile[i];
+        ks[u] = me.ks[i];
+        const float vs = me.vs[i];
+        lv[u] = __log2f(vs);
+        iv[u] = __fdividef(1.0f / kShift<FMT>, vs);   // (O holds codes / kShift)
+      }
+      // S = K q^T
+      float sc[N][NT][4];
+#pragma unroll
+      for (int u = 0; u < N; ++u)
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt) sc[u][nt][0] = sc[u][nt][1] = sc[u][nt][2] = sc[u][nt][3] = 0.0f;
 #pragma unroll
       for (int i = 0; i < D / 64; ++i) {
-        uint4 lo, hi;
-        if constexpr (D == 128) {
-          const int c = ((2 * t + i) ^ g) << 4;
-          lo = *reinterpret_cast<const uint4*>(kt + g * 128 + c);
-          hi = *reinterpret_cast<const uint4*>(kt + (g + 8) * 128 + c);
-        } else {
-          const int c = (t ^ (g >> 1)) << 4;
-          lo = *reinterpret_cast<const uint4*>(kt + g * 64 + c);
-          hi = *reinterpret_cast<const uint4*>(kt + (g + 8) * 64 + c);
-        }
-        const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
+        const int c = D == 128 ? ((2 * t + i) ^ g) << 4 : (t ^ (g >> 1)) << 4;
 #pragma unroll
-        for (int w = 0; w < 4; ++w) {
-          const uint32_t a[4] = {code_even<FMT>(wl[w]), code_even<FMT>(wh[w]), code_odd<FMT>(wl[w]),
-                                 code_odd<FMT>(wh[w])};
+        for (int u = 0; u < N; ++u) {
+          const uint4 lo = *reinterpret_cast<const uint4*>(kt[u] + g * D + c);
+          const uint4 hi = *reinterpret_cast<const uint4*>(kt[u] + (g + 8) * D + c);
+          const uint32_t wl[4] = {lo.x, lo.y, lo.z, lo.w}, wh[4] = {hi.x, hi.y, hi.z, hi.w};
 #pragma unroll
-          for (int nt = 0; nt < NT; ++nt) mma_16816(sc[nt], a, qf[nt][8 * i + 2 * w], qf[nt][8 * i + 2 * w + 1]);
+          for (int w = 0; w < 4; ++w) {
+            const uint32_t a[4] = {code_even<FMT>(wl[w]), code_even<FMT>(wh[w]), code_odd<FMT>(wl[w]),
+                                   code_odd<FMT>(wh[w])};
+#pragma unroll
+            for (int nt = 0; nt < NT; ++nt) mma_16816(sc[u][nt], a, qf[nt][8 * i + 2 * w], qf[nt][8 * i + 2 * w + 1]);
+          }
         }
       }
       // weights
-      const float lv = __log2f(vs), iv = __fdividef(1.0f / kShift<FMT>, vs);   // (O holds codes / kShift)
-      const bool all = tile + kBlock - 1 <= p_low &&
-                       (p.window == 0 || tile > p_high - p.window || tile + kBlock <= p.sinks);
       bool raise = false;
 #pragma unroll
-      for (int nt = 0; nt < NT; ++nt)
+      for (int u = 0; u < N; ++u) {
+        const bool all = tile[u] + kBlock - 1 <= p_low &&
+                         (p.window == 0 || tile[u] > p_high - p.window || tile[u] + kBlock <= p.sinks);
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          float v = fmaf(sc[nt][e], factor[nt][e & 1] * ks, lv);
-          if (!all) {
-            const int j = tile + g + (e & 2) * 4, q = at[nt][e & 1];
-            if (!(j <= q && (p.window == 0 || j > q - p.window || j < p.sinks))) v = -INFINITY;
-          }
-          sc[nt][e] = v;
-          raise |= v > m[nt][e & 1] + kSlack;
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 4; ++e) sc[u][nt][e] = fmaf(sc[u][nt][e], factor[nt][e & 1] * ks[u], lv[u]);
+        if (!all) {
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+              const int j = tile[u] + g + (e & 2) * 4, q = at[nt][e & 1];
+              if (!(j <= q && (p.window == 0 || j > q - p.window || j < p.sinks))) sc[u][nt][e] = -INFINITY;
+            }
         }
+#pragma unroll
+        for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+          for (int e = 0; e < 2; ++e) raise |= fmaxf(sc[u][nt][e], sc[u][nt][e + 2]) > m[nt][e] + kSlack;
+      }
       if (__any_sync(0xffffffffu, raise)) {
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
           for (int e = 0; e < 2; ++e) {
-            float v = fmaxf(sc[nt][e], sc[nt][e + 2]);
+            float v = m[nt][e];
+#pragma unroll
+            for (int u = 0; u < N; ++u) v = fmaxf(v, fmaxf(sc[u][nt][e], sc[u][nt][e + 2]));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 4));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 8));
             v = fmaxf(v, __shfl_xor_sync(0xffffffffu, v, 16));
-            v = fmaxf(v, m[nt][e]);
             const float f = v == -INFINITY ? 1.0f : exp2_fast(m[nt][e] - v);
             m[nt][e] = v;
             l[nt][e] *= f;
@@ -529,48 +551,70 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             }
           }
       }
-      uint32_t b0[NT], b1[NT];
+      uint32_t b0[N][NT], b1[N][NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        float w[4];
+        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
 #pragma unroll
-        for (int e = 0; e < 4; ++e) {
-          const float mm = m[nt][e & 1];
-          w[e] = exp2_fast(sc[nt][e] - (mm == -INFINITY ? 0.0f : mm));
-          l[nt][e & 1] = fmaf(w[e], iv, l[nt][e & 1]);
+        for (int u = 0; u < N; ++u) {
+          float w[4];
+#pragma unroll
+          for (int e = 0; e < 4; ++e) w[e] = exp2_fast(sc[u][nt][e] - base[e & 1]);
+          l[nt][0] = fmaf(w[0] + w[2], iv[u], l[nt][0]);
+          l[nt][1] = fmaf(w[1] + w[3], iv[u], l[nt][1]);
+          b0[u][nt] = transpose8x8(Half16<__half>::pack(w[0], w[1]));
+          b1[u][nt] = transpose8x8(Half16<__half>::pack(w[2], w[3]));
         }
-        b0[nt] = transpose8x8(Half16<__half>::pack(w[0], w[1]));
-        b1[nt] = transpose8x8(Half16<__half>::pack(w[2], w[3]));
       }
       // O += V^T p: lane (g, t) holds channels [D/8 g, D/8 (g + 1)) of keys 2t, 2t+1, 2t+8, 2t+9
-      uint32_t vw[4][D / 32];
 #pragma unroll
-      for (int i = 0; i < 4; ++i) {
-        const int r = 2 * t + (i & 1) + (i >> 1) * 8;
-        if constexpr (D == 128) {
-          const uint4 x = *reinterpret_cast<const uint4*>(vt + r * 128 + ((g ^ (r & 7)) << 4));
-          vw[i][0] = x.x;
-          vw[i][1] = x.y;
-          vw[i][2] = x.z;
-          vw[i][3] = x.w;
-        } else {
-          const uint2 x = *reinterpret_cast<const uint2*>(vt + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
-          vw[i][0] = x.x;
-          vw[i][1] = x.y;
+      for (int u = 0; u < N; ++u) {
+        uint32_t vw[4][D / 32];
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+          const int r = 2 * t + (i & 1) + (i >> 1) * 8;
+          if constexpr (D == 128) {
+            const uint4 x = *reinterpret_cast<const uint4*>(vt[u] + r * 128 + ((g ^ (r & 7)) << 4));
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+            vw[i][2] = x.z;
+            vw[i][3] = x.w;
+          } else {
+            const uint2 x =
+                *reinterpret_cast<const uint2*>(vt[u] + r * 64 + (((g >> 1) ^ ((r >> 1) & 3)) << 4) + (g & 1) * 8);
+            vw[i][0] = x.x;
+            vw[i][1] = x.y;
+          }
+        }
+#pragma unroll
+        for (int w = 0; w < D / 32; ++w) {
+          // two channels of two keys to a word
+          const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
+          const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
+          const uint32_t a0[4] = {code_even<FMT>(x0), code_odd<FMT>(x0), code_even<FMT>(x1), code_odd<FMT>(x1)};
+          const uint32_t a1[4] = {code_even<FMT>(y0), code_odd<FMT>(y0), code_even<FMT>(y1), code_odd<FMT>(y1)};
+#pragma unroll
+          for (int nt = 0; nt < NT; ++nt) {
+            mma_16816(acc[nt][2 * w], a0, b0[u][nt], b1[u][nt]);
+            mma_16816(acc[nt][2 * w + 1], a1, b0[u][nt], b1[u][nt]);
+          }
         }
       }
+    };
+    {
+      bool here[U];
+      bool both = true;
 #pragma unroll
-      for (int w = 0; w < D / 32; ++w) {
-        // two channels of two keys to a word
-        const uint32_t x0 = __byte_perm(vw[0][w], vw[1][w], 0x5410), y0 = __byte_perm(vw[0][w], vw[1][w], 0x7632);
-        const uint32_t x1 = __byte_perm(vw[2][w], vw[3][w], 0x5410), y1 = __byte_perm(vw[2][w], vw[3][w], 0x7632);
-        const uint32_t a0[4] = {code_even<FMT>(x0), code_odd<FMT>(x0), code_even<FMT>(x1), code_odd<FMT>(x1)};
-        const uint32_t a1[4] = {code_even<FMT>(y0), code_odd<FMT>(y0), code_even<FMT>(y1), code_odd<FMT>(y1)};
-#pragma unroll
-        for (int nt = 0; nt < NT; ++nt) {
-          mma_16816(acc[nt][2 * w], a0, b0[nt], b1[nt]);
-          mma_16816(acc[nt][2 * w + 1], a1, b0[nt], b1[nt]);
-        }
+      for (int u = 0; u < U; ++u) {
+        here[u] = me.tile[warp + u * W] >= 0;
+        both &= here[u];
+      }
+      if (both) {
+        take(std::integral_constant<int, U>{}, warp);
+      } else {
+#pragma unroll 1
+        for (int u = 0; u < U; ++u)
+          if (me.tile[warp + u * W] >= 0) take(std::integral_constant<int, 1>{}, warp + u * W);
       }
     }
     __syncwarp();
@@ -811,7 +855,7 @@ awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, i
   // No more CTAs than the longest sequences that fit could give work to.
   const int64_t tiles = (int64_t(batch->max_pages) * cache->page_size + kBlock - 1) / kBlock + 1;
   const int64_t work = plan->many ? (tiles + 7) / 8 * ((n_tokens * group + kPairRows - 1) / kPairRows + batch->n_seqs)
-                                  : (tiles + W - 1) / W * ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs);
+                                  : (tiles + WT - 1) / WT * ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs);
   if (work <= plan->grid / cache->n_kv_heads) plan->grid = int(work > 0 ? work : 1) * cache->n_kv_heads;
   return AWQ_OK;
 }
