@@ -108,7 +108,6 @@ template <int D, int R>
 struct Shared {
   static constexpr int kTile = kBlock * D;              // bytes of 16 keys or values
   static constexpr int kStageBytes = 2 * WT * kTile;
-  static constexpr int kMergeRow = D + 4;
   struct Meta {
     int tile[WT];           // position of the tile's first key, -1: nothing there
     float ks[WT], vs[WT];
@@ -119,11 +118,10 @@ struct Shared {
   };
   uint8_t ring[kStages][kStageBytes];
   uint8_t q[kStages][R * D * 2];               // the item's q rows, in its first stage
-  float merge[W][R][kMergeRow];
-  float stat[W][R][2];
+  float2 stat[2][W][R];                        // [merge parity][warp][row]: m, l
   Meta meta[kStages];
   Item items[kItems];
-  uint64_t full[kStages], empty[kStages], merged, taken;
+  uint64_t full[kStages], empty[kStages], merged;
   int64_t scratch[40];
   int abort;
 };
@@ -242,7 +240,7 @@ __device__ __forceinline__ void load_q(const uint8_t* row, int t, uint32_t (&f)[
 }
 
 template <typename T, int D, int FMT, int NT>
-__global__ void __launch_bounds__(kThreads, 2)
+__global__ void __launch_bounds__(kThreads, NT == 2 ? 2 : D == 64 ? 4 : 3)
 decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_constant__ CUtensorMap map_v,
                         const __grid_constant__ AttentionParams p) {
   constexpr int R = 8 * NT;
@@ -259,7 +257,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       mbar_init(&sh.empty[i], W);
     }
     mbar_init(&sh.merged, W);
-    mbar_init(&sh.taken, W);
     sh.abort = 0;
     asm volatile("fence.mbarrier_init.release.cluster;" ::: "memory");
     fence_proxy_async_smem();
@@ -609,13 +606,74 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         here[u] = me.tile[warp + u * W] >= 0;
         both &= here[u];
       }
-      if (both) {
-        take(std::integral_constant<int, U>{}, warp);
+      if (NT == 1 && both) {   // (two tiles of two column groups would not fit the registers)
+        take(std::integral_constant<int, NT == 1 ? U : 1>{}, warp);
       } else {
 #pragma unroll 1
         for (int u = 0; u < U; ++u)
           if (me.tile[warp + u * W] >= 0) take(std::integral_constant<int, 1>{}, warp + u * W);
       }
+    }
+    if (flags & 2) {
+      // The item's end: the warps join their parts, each in the place of its own tiles of this stage (four rows to a
+      // tile), which is given back when all have read them.
+      auto part = [&](int w, int r) {
+        return reinterpret_cast<float*>(&sh.ring[s][((r >> 3) * WT + w + ((r >> 2) & 1) * W) * Sh::kTile]) + (r & 3) * D;
+      };
+      float2(*stat)[R] = sh.stat[merges & 1];
+      __syncwarp();
+#pragma unroll
+      for (int nt = 0; nt < NT; ++nt)
+#pragma unroll
+        for (int e = 0; e < 2; ++e) {
+          const int r = nt * 8 + 2 * t + e;
+          float sum = l[nt][e];
+          sum += __shfl_xor_sync(0xffffffffu, sum, 4);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 8);
+          sum += __shfl_xor_sync(0xffffffffu, sum, 16);
+          if (g == 0) stat[warp][r] = make_float2(m[nt][e], sum);
+          if (r < rows) {
+            float* dst = part(warp, r) + D / 8 * g;
+#pragma unroll
+            for (int j = 0; j < D / 16; ++j)
+              *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
+          }
+        }
+      __syncwarp();
+      if (lane == 0) mbar_arrive(&sh.merged);
+      if (!wait(&sh.merged, merges & 1)) return;
+      ++merges;
+      for (int i = threadIdx.x; i < rows * (D / 4); i += W * 32) {
+        const int r = i / (D / 4), d = i % (D / 4) * 4;
+        float top = -INFINITY;
+#pragma unroll
+        for (int w = 0; w < W; ++w) top = fmaxf(top, stat[w][r].x);
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.0f;
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+          const float f = top == -INFINITY ? 0.0f : exp2_fast(stat[w][r].x - top);
+          const float4 x = *reinterpret_cast<const float4*>(part(w, r) + d);
+          sum = fmaf(f, stat[w][r].y, sum);
+          o.x = fmaf(f, x.x, o.x);
+          o.y = fmaf(f, x.y, o.y);
+          o.z = fmaf(f, x.z, o.z);
+          o.w = fmaf(f, x.w, o.w);
+        }
+        if (dest < 0) {
+          const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
+          const int row = row0 + r;
+          uint16_t* dst = p.out + int64_t(t0 + row / p.group) * p.out_stride +
+                          int64_t(head * p.group + row % p.group) * D + d;
+          *reinterpret_cast<uint2*>(dst) =
+              make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
+        } else {
+          float* out = p.part + int64_t(dest) * (R * (D + 2));
+          *reinterpret_cast<float4*>(out + r * D + d) = o;
+          if (d == 0) *reinterpret_cast<float2*>(out + R * D + 2 * r) = make_float2(top, sum);
+        }
+      }
+      fence_proxy_async_smem();   // the next copy comes behind these writes and reads
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[s]);
@@ -624,66 +682,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       s = 0;
       ph ^= 1;
     }
-    if (!(flags & 2)) continue;
-
-    // join the warps' parts of the item
-    if (merges && !wait(&sh.taken, (merges - 1) & 1)) return;
-#pragma unroll
-    for (int nt = 0; nt < NT; ++nt)
-#pragma unroll
-      for (int e = 0; e < 2; ++e) {
-        const int r = nt * 8 + 2 * t + e;
-        float sum = l[nt][e];
-        sum += __shfl_xor_sync(0xffffffffu, sum, 4);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 8);
-        sum += __shfl_xor_sync(0xffffffffu, sum, 16);
-        if (g == 0) {
-          sh.stat[warp][r][0] = m[nt][e];
-          sh.stat[warp][r][1] = sum;
-        }
-        if (r < rows) {
-#pragma unroll
-          for (int j = 0; j < D / 16; ++j)
-            *reinterpret_cast<float2*>(&sh.merge[warp][r][D / 8 * g + 2 * j]) =
-                make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
-        }
-      }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.merged);
-    if (!wait(&sh.merged, merges & 1)) return;
-    for (int i = threadIdx.x; i < rows * (D / 4); i += W * 32) {
-      const int r = i / (D / 4), d = i % (D / 4) * 4;
-      float top = -INFINITY;
-#pragma unroll
-      for (int w = 0; w < W; ++w) top = fmaxf(top, sh.stat[w][r][0]);
-      float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-      float sum = 0.0f;
-#pragma unroll
-      for (int w = 0; w < W; ++w) {
-        const float f = top == -INFINITY ? 0.0f : exp2_fast(sh.stat[w][r][0] - top);
-        const float4 x = *reinterpret_cast<const float4*>(&sh.merge[w][r][d]);
-        sum = fmaf(f, sh.stat[w][r][1], sum);
-        o.x = fmaf(f, x.x, o.x);
-        o.y = fmaf(f, x.y, o.y);
-        o.z = fmaf(f, x.z, o.z);
-        o.w = fmaf(f, x.w, o.w);
-      }
-      if (dest < 0) {
-        const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
-        const int row = row0 + r;
-        uint16_t* dst = p.out + int64_t(t0 + row / p.group) * p.out_stride +
-                        int64_t(head * p.group + row % p.group) * D + d;
-        *reinterpret_cast<uint2*>(dst) =
-            make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
-      } else {
-        float* part = p.part + int64_t(dest) * (R * (D + 2));
-        *reinterpret_cast<float4*>(part + r * D + d) = o;
-        if (d == 0) *reinterpret_cast<float2*>(part + R * D + 2 * r) = make_float2(top, sum);
-      }
-    }
-    __syncwarp();
-    if (lane == 0) mbar_arrive(&sh.taken);
-    ++merges;
   }
 }
 
