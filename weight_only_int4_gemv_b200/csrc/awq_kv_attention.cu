@@ -69,6 +69,7 @@ struct AttentionParams {
   float scale_log2;
   int32_t window, sinks;
   int32_t group, n_kv_heads;
+  int32_t whole;                           // few rows: a CTA takes whole items (no parts, no join)
   float* part;                             // [2 grid][R][D + 2] fp32
   struct Join* joins;                      // [grid]
 };
@@ -274,11 +275,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       p.batch.n_seqs, sh.scratch,
       [&](int b) {
         const Span a = span_of<R>(p, load_seq(p.batch, b, err));
-        return int64_t(a.tiles) * a.row_tiles * p.n_kv_heads;
+        return int64_t(p.whole ? 1 : a.tiles) * a.row_tiles * p.n_kv_heads;
       },
       [&](int64_t sum) {
         per = (sum + gridDim.x - 1) / gridDim.x;
-        per = (per + WT - 1) / WT * WT;
         return per * blockIdx.x;
       },
       &rest, &total);
@@ -295,7 +295,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       int b = b_first;
       Seq seq = load_seq(p.batch, b, err);
       Span a = span_of<R>(p, seq);
-      int item = int(rest / a.tiles), tile = int(rest % a.tiles), items = a.row_tiles * p.n_kv_heads, left = int(u1 - u0);
+      int item = p.whole ? int(rest) : int(rest / a.tiles), tile = p.whole ? 0 : int(rest % a.tiles);
+      int items = a.row_tiles * p.n_kv_heads, left = int(u1 - u0);   // left: units of this run
       const int32_t* table = p.batch.table + int64_t(b) * p.batch.table_stride;
       uint32_t n_items = 0;
       bool fresh = true;             // the next stage begins an item, or this run
@@ -303,7 +304,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       // One stage ahead of the copies: the tiles of the next stage, and the loads of its pages' ids. lane i < WT: tile
       // i's keys, lane WT + i: its values. What an item's stages share goes to a ring of its own.
       struct Stage {
-        int flags, pos, id;          // flags: first | last << 1 | count << 2 | item's place << 8
+        int flags, pos, id;          // flags: first | last << 1 | the run's last << 2 | item's place << 8
       };
       auto next = [&](Stage& st) {
         if (fresh) {
@@ -316,7 +317,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
           }
           const int row_tile = item / p.n_kv_heads;
           const int64_t begin = u1 - left - tile, end = begin + a.tiles;
-          const int dest = begin >= u0 && end <= u1 ? -1 : int(2 * blockIdx.x) + (begin > u0);
+          const bool split = !p.whole && (begin < u0 || end > u1);
+          const int dest = split ? int(2 * blockIdx.x) + (begin > u0) : -1;
           ++n_items;
           auto& it = sh.items[n_items % kItems];
           const int row0 = row_tile * R, rows = min(R, seq.n * p.group - row0), head = item - row_tile * p.n_kv_heads;
@@ -328,7 +330,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             it.head = head;
             it.dest = dest;
           }
-          if (begin >= u0 && end > u1) {
+          if (split && begin >= u0) {
             join.last = int((end - 1) / per);
             join.slot = dest;
             join.t0 = seq.t0;
@@ -337,8 +339,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             join.head = head;
           }
         }
-        const int rem = min(a.tiles - tile, left), cnt = min(WT, rem), v = tile + i;
-        st.flags = int(fresh) | (rem <= WT ? 2 : 0) | cnt << 2 | int(n_items % kItems) << 8;
+        const int rem = p.whole ? a.tiles - tile : min(a.tiles - tile, left), cnt = min(WT, rem), v = tile + i;
+        const int first = fresh;
+        tile += cnt;
+        fresh = tile == a.tiles;
+        left -= p.whole ? int(fresh) : cnt;
+        st.flags = first | (rem <= WT ? 2 : 0) | (left == 0 ? 4 : 0) | int(n_items % kItems) << 8;
         st.pos = -1;
         st.id = -1;
         if (lane < 2 * WT && i < cnt) {
@@ -348,9 +354,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             st.id = table[pos / p.batch.page_size];
           }
         }
-        left -= cnt;
-        tile += cnt;
-        fresh = tile == a.tiles;
         if (fresh) {
           tile = 0;
           ++item;
@@ -411,7 +414,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         cur = after;
       }
     }
-    if (lane == 0) p.joins[blockIdx.x] = join;
+    if (lane == 0 && !p.whole) p.joins[blockIdx.x] = join;
     if (!ok) {
       // every copy issued lands before the CTA's shared memory goes
       for (int k = 0; k < kStages; ++k)
@@ -431,7 +434,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   int t0 = 0, row0 = 0, rows = 0, head = 0, dest = 0;
   int s = 0;
   uint32_t ph = 0, merges = 0;
-  for (int64_t u = u0; u < u1;) {
+  for (bool more = b_first >= 0; more;) {
     if (!wait(&sh.full[s], ph)) return;
     const auto& me = sh.meta[s];
     const int flags = me.flags;
@@ -462,9 +465,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       p_low = past + row0 / p.group;
       p_high = past + (row0 + rows - 1) / p.group;
     }
-    // N tiles of the warp together, W apart: their loads, products and exponentials overlap
+    // N tiles of the warp together, W apart: their loads, products and exponentials overlap. Where the stage has
+    // only some of them the others' weights are 0 (one path for all keeps the code in the instruction cache).
     auto take = [&](auto count, int first) {
       constexpr int N = decltype(count)::value;
+      if (me.tile[first] < 0) return;
       const uint8_t* kt[N];
       const uint8_t* vt[N];
       int tile[N];
@@ -475,8 +480,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         kt[u] = &sh.ring[s][i * Sh::kTile];
         vt[u] = &sh.ring[s][(WT + i) * Sh::kTile];
         tile[u] = me.tile[i];
-        ks[u] = me.ks[i];
-        const float vs = me.vs[i];
+        ks[u] = tile[u] < 0 ? 0.0f : me.ks[i];
+        const float vs = tile[u] < 0 ? 1.0f : me.vs[i];
         lv[u] = __log2f(vs);
         iv[u] = __fdividef(1.0f / kShift<FMT>, vs);   // (O holds codes / kShift)
       }
@@ -507,7 +512,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       bool raise = false;
 #pragma unroll
       for (int u = 0; u < N; ++u) {
-        const bool all = tile[u] + kBlock - 1 <= p_low &&
+        const bool all = tile[u] >= 0 && tile[u] + kBlock - 1 <= p_low &&
                          (p.window == 0 || tile[u] > p_high - p.window || tile[u] + kBlock <= p.sinks);
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
@@ -519,7 +524,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
               const int j = tile[u] + g + (e & 2) * 4, q = at[nt][e & 1];
-              if (!(j <= q && (p.window == 0 || j > q - p.window || j < p.sinks))) sc[u][nt][e] = -INFINITY;
+              if (!(tile[u] >= 0 && j <= q && (p.window == 0 || j > q - p.window || j < p.sinks)))
+                sc[u][nt][e] = -INFINITY;
             }
         }
 #pragma unroll
@@ -598,22 +604,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         }
       }
     };
-    {
-      bool here[U];
-      bool both = true;
-#pragma unroll
-      for (int u = 0; u < U; ++u) {
-        here[u] = me.tile[warp + u * W] >= 0;
-        both &= here[u];
-      }
-      if (NT == 1 && both) {   // (two tiles of two column groups would not fit the registers)
-        take(std::integral_constant<int, NT == 1 ? U : 1>{}, warp);
-      } else {
+    // (two tiles of two column groups would not fit the registers)
+    constexpr int N = NT == 1 ? U : 1;
 #pragma unroll 1
-        for (int u = 0; u < U; ++u)
-          if (me.tile[warp + u * W] >= 0) take(std::integral_constant<int, 1>{}, warp + u * W);
-      }
-    }
+    for (int u = 0; u < U; u += N) take(std::integral_constant<int, N>{}, warp + u * W);
     if (flags & 2) {
       // The item's end: the warps join their parts, each in the place of its own tiles of this stage (four rows to a
       // tile), which is given back when all have read them.
@@ -677,7 +671,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     }
     __syncwarp();
     if (lane == 0) mbar_arrive(&sh.empty[s]);
-    u += (flags >> 2) & 63;
+    more = !(flags & 4);
     if (++s == kStages) {
       s = 0;
       ph ^= 1;
@@ -835,9 +829,16 @@ awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* 
 
 struct Plan {
   Variant v;
-  bool many;
+  bool many, whole;
   int grid;
 };
+
+// Up to how many tiles an item is taken whole by one CTA, without parts and the kernel that joins them, when there is
+// a CTA for every item. Measured (32 / 8 heads of 128, int8; whole and split, us):
+//   1 sequence of 128, 500, 1000 tokens:   5.6 and 6.9, 9.5 and 7.9, 15 and 10
+//   8 sequences of up to 128, 500, 1000:   6.8 and 10, 10 and 12, 16 and 12
+//   32 sequences of up to 128, 500, 1000:  7.7 and 13, 12 and 17, 19 and 20
+int whole_tiles(int64_t items, int grid) { return items > grid ? 0 : items * 2 >= grid ? 64 : items * 8 >= grid ? 40 : 24; }
 
 awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens, int32_t dtype,
                      int32_t n_q_heads, Plan* plan) {
@@ -851,10 +852,15 @@ awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, i
   const awq_status_t st = resident(plan->v, key, &plan->grid);
   if (st != AWQ_OK) return st;
   // No more CTAs than the longest sequences that fit could give work to.
-  const int64_t tiles = (int64_t(batch->max_pages) * cache->page_size + kBlock - 1) / kBlock + 1;
+  const int64_t tiles = int64_t(batch->max_pages) * (cache->page_size / kBlock) + 1;
   const int64_t work = plan->many ? (tiles + 7) / 8 * ((n_tokens * group + kPairRows - 1) / kPairRows + batch->n_seqs)
                                   : (tiles + WT - 1) / WT * ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs);
-  if (work <= plan->grid / cache->n_kv_heads) plan->grid = int(work > 0 ? work : 1) * cache->n_kv_heads;
+  const int64_t items = ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs) * cache->n_kv_heads;
+  plan->whole = !plan->many && tiles <= whole_tiles(items, plan->grid);
+  if (plan->whole)
+    plan->grid = int(items);
+  else if (work <= plan->grid / cache->n_kv_heads)
+    plan->grid = int(work > 0 ? work : 1) * cache->n_kv_heads;
   return AWQ_OK;
 }
 
@@ -928,6 +934,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   p.sinks = p.window ? sinks : 0;
   p.group = n_q_heads / cache->n_kv_heads;
   p.n_kv_heads = cache->n_kv_heads;
+  p.whole = plan.whole;
   p.joins = static_cast<Join*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + size_t(plan.grid) * sizeof(Join));
 
@@ -950,7 +957,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   cudaLaunchAttribute attr;
   cudaLaunchConfig_t lc = overlapped(dim3(unsigned(plan.grid)), plan.v.threads, plan.v.smem, stream, &attr);
   cudaError_t e = cudaLaunchKernelEx(&lc, plan.v.main, map_k, map_v, p);
-  if (e == cudaSuccess) {
+  if (e == cudaSuccess && !plan.whole) {
     lc = overlapped(dim3(unsigned(plan.grid), plan.v.join_grid.y), plan.v.join_threads, 0, stream, &attr);
     e = cudaLaunchKernelEx(&lc, plan.v.join, p);
   }
