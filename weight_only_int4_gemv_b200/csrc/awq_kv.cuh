@@ -116,6 +116,12 @@ inline Batch make_batch(const awq_kv_cache_t* c, const awq_kv_batch_t* b, int64_
   return r;
 }
 
+// a / b for a >= 0, b > 0: 64-bit division takes several hundred cycles, and
+// both are nearly always short.
+__device__ __forceinline__ int64_t divide(int64_t a, int64_t b) {
+  return (uint64_t(a | b) >> 32) ? a / b : int64_t(uint32_t(a) / uint32_t(b));
+}
+
 // One sequence: its tokens of this call are rows t0 .. t0 + n - 1, at
 // positions past .. len - 1 (past is negative when the sequence is shorter
 // than its rows: those rows have no position). The values come from device

@@ -54,6 +54,9 @@ constexpr int kThreads = (W + 1) * 32;
 constexpr int U = 2;                       // tiles of a warp in a stage
 constexpr int WT = W * U;                  // tiles of a stage
 constexpr int kStages = 2;
+// What an item costs a CTA beyond its tiles (q rows, the warps' joining, output), in tiles: the cut counts every item
+// as that much longer.
+constexpr int kItemCost = 12;
 constexpr int kItems = 8;                  // more than the stages in the ring and the one ahead of it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
@@ -69,6 +72,7 @@ struct AttentionParams {
   float scale_log2;
   int32_t window, sinks;
   int32_t group, n_kv_heads;
+  float inv_group;
   int32_t whole;                           // few rows: a CTA takes whole items (no parts, no join)
   float* part;                             // [2 grid][R][D + 2] fp32
   struct Join* joins;                      // [grid]
@@ -115,6 +119,7 @@ struct Shared {
     int flags;
   };
   struct Item {
+    int tok0, rem0;         // the token of its first row, and that row's head in the group
     int t0, row0, rows, past, head, dest;
   };
   uint8_t ring[kStages][kStageBytes];
@@ -269,16 +274,19 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
   };
 
+  // row / group for the rows of a tile, counted from a token's first (below 2^17: a float's product is exact enough)
+  auto by_group = [&](int row) { return int((float(row) + 0.5f) * p.inv_group); };
+
   // this CTA's run of units
   int64_t per = 0, total = 0, rest = 0;
   const int b_first = locate(
       p.batch.n_seqs, sh.scratch,
       [&](int b) {
         const Span a = span_of<R>(p, load_seq(p.batch, b, err));
-        return int64_t(p.whole ? 1 : a.tiles) * a.row_tiles * p.n_kv_heads;
+        return int64_t(p.whole ? 1 : a.tiles + kItemCost) * a.row_tiles * p.n_kv_heads;
       },
       [&](int64_t sum) {
-        per = (sum + gridDim.x - 1) / gridDim.x;
+        per = divide(sum + gridDim.x - 1, gridDim.x);
         return per * blockIdx.x;
       },
       &rest, &total);
@@ -295,11 +303,15 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       int b = b_first;
       Seq seq = load_seq(p.batch, b, err);
       Span a = span_of<R>(p, seq);
-      int item = p.whole ? int(rest) : int(rest / a.tiles), tile = p.whole ? 0 : int(rest % a.tiles);
-      int items = a.row_tiles * p.n_kv_heads, left = int(u1 - u0);   // left: units of this run
+      // An item's units are its cost, then its tiles (whole items: one unit). rel: the current item's first unit,
+      // counted from the run's; tile .. end: its tiles of this run.
+      const int run = int(u1 - u0), width = p.whole ? 1 : a.tiles + kItemCost;
+      int item = int(divide(rest, width)), rel = int(int64_t(item) * width - rest), tile = 0, end = 0;
+      int items = a.row_tiles * p.n_kv_heads;
       const int32_t* table = p.batch.table + int64_t(b) * p.batch.table_stride;
       uint32_t n_items = 0;
       bool fresh = true;             // the next stage begins an item, or this run
+      bool more = p.whole || max(rel + kItemCost, 0) < run;   // there is a next stage
       const int i = lane % WT;
       // One stage ahead of the copies: the tiles of the next stage, and the loads of its pages' ids. lane i < WT: tile
       // i's keys, lane WT + i: its values. What an item's stages share goes to a ring of its own.
@@ -315,14 +327,19 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             items = a.row_tiles * p.n_kv_heads;
             table = p.batch.table + int64_t(b) * p.batch.table_stride;
           }
-          const int row_tile = item / p.n_kv_heads;
-          const int64_t begin = u1 - left - tile, end = begin + a.tiles;
-          const bool split = !p.whole && (begin < u0 || end > u1);
-          const int dest = split ? int(2 * blockIdx.x) + (begin > u0) : -1;
+          const int first = rel + kItemCost, row_tile = item / p.n_kv_heads;
+          tile = p.whole ? 0 : max(-first, 0);
+          end = p.whole ? a.tiles : min(run - first, a.tiles);
+          const bool split = tile > 0 || end < a.tiles;
+          // a part that starts its item goes to the CTA's second place, one that continues it to the first
+          const int dest = split ? int(2 * blockIdx.x) + (tile == 0) : -1;
           ++n_items;
           auto& it = sh.items[n_items % kItems];
           const int row0 = row_tile * R, rows = min(R, seq.n * p.group - row0), head = item - row_tile * p.n_kv_heads;
+          const int tok0 = row0 / p.group;
           if (lane == 0) {
+            it.tok0 = tok0;
+            it.rem0 = row0 - tok0 * p.group;
             it.t0 = seq.t0;
             it.row0 = row0;
             it.rows = rows;
@@ -330,8 +347,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             it.head = head;
             it.dest = dest;
           }
-          if (split && begin >= u0) {
-            join.last = int((end - 1) / per);
+          if (split && tile == 0) {
+            join.last = int(divide(u0 + first + a.tiles - 1, per));
             join.slot = dest;
             join.t0 = seq.t0;
             join.row0 = row0;
@@ -339,12 +356,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             join.head = head;
           }
         }
-        const int rem = p.whole ? a.tiles - tile : min(a.tiles - tile, left), cnt = min(WT, rem), v = tile + i;
-        const int first = fresh;
+        const int cnt = min(WT, end - tile), v = tile + i, first = fresh;
         tile += cnt;
-        fresh = tile == a.tiles;
-        left -= p.whole ? int(fresh) : cnt;
-        st.flags = first | (rem <= WT ? 2 : 0) | (left == 0 ? 4 : 0) | int(n_items % kItems) << 8;
+        fresh = tile == end;
+        if (fresh) rel += p.whole ? 1 : a.tiles + kItemCost;
+        more = !fresh || (p.whole ? rel < run : rel + kItemCost < run);
+        st.flags = first | int(fresh) << 1 | int(!more) << 2 | int(n_items % kItems) << 8;
         st.pos = -1;
         st.id = -1;
         if (lane < 2 * WT && i < cnt) {
@@ -354,17 +371,14 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
             st.id = table[pos / p.batch.page_size];
           }
         }
-        if (fresh) {
-          tile = 0;
-          ++item;
-        }
+        if (fresh) ++item;
       };
-      Stage cur, after;
-      bool more = left > 0;
+      Stage cur = {4, -1, -1}, after;  // (a run that ends within an item's cost: one stage without tiles)
+      bool go = true;
       if (more) next(cur);
-      while (more) {
-        more = left > 0;
-        if (more) next(after);
+      while (go) {
+        go = more;
+        if (go) next(after);
         if (!wait(&sh.empty[s], ph ^ 1)) {
           ok = false;
           break;
@@ -392,14 +406,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         if (cur.flags & 1) {             // the item's q rows, zeros behind its last
           constexpr int CPR = D / 8;
           const uint32_t dst = smem_u32(sh.q[s]);
-          const int t0 = it.t0, row0 = it.row0, rows = it.rows, head = it.head;
+          const int t0 = it.t0 + it.tok0, rem0 = it.rem0, rows = it.rows, head0 = it.head * p.group;
 #pragma unroll
           for (int c = lane; c < R * CPR; c += 32) {
-            const int r = c / CPR, row = row0 + r, tok = row / p.group;
+            const int r = c / CPR, row = rem0 + r, tok = by_group(row);
             const bool there = r < rows;
             const uint16_t* src = p.q;
-            if (there)
-              src += int64_t(t0 + tok) * p.q_stride + int64_t(head * p.group + row - tok * p.group) * D + (c % CPR) * 8;
+            if (there) src += int64_t(t0 + tok) * p.q_stride + int64_t(head0 + row - tok * p.group) * D + (c % CPR) * 8;
             asm volatile("cp.async.cg.shared.global [%0], [%1], 16, %2;" ::"r"(dst + c * 16), "l"(src),
                          "r"(there ? 16 : 0)
                          : "memory");
@@ -431,7 +444,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   float m[NT][2], l[NT][2];
   float acc[NT][D / 16][4];
   int p_low = 0, p_high = 0;         // the lowest and highest of them
-  int t0 = 0, row0 = 0, rows = 0, head = 0, dest = 0;
+  int t0 = 0, rem0 = 0, rows = 0, head = 0, dest = 0;   // t0: the token of the item's first row
   int s = 0;
   uint32_t ph = 0, merges = 0;
   for (bool more = b_first >= 0; more;) {
@@ -440,12 +453,12 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     const int flags = me.flags;
     if (flags & 1) {
       const auto& it = sh.items[flags >> 8];
-      t0 = it.t0;
-      row0 = it.row0;
+      t0 = it.t0 + it.tok0;
+      rem0 = it.rem0;
       rows = it.rows;
       head = it.head;
       dest = it.dest;
-      const int past = it.past;
+      const int past = it.past + it.tok0;
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
         float mine;
@@ -453,7 +466,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
           factor[nt][e] = p.scale_log2 * kShift<FMT> * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
-          at[nt][e] = past + (row0 + nt * 8 + 2 * t + e) / p.group;
+          at[nt][e] = past + by_group(rem0 + nt * 8 + 2 * t + e);
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.0f;
         }
@@ -462,8 +475,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
           for (int e = 0; e < 4; ++e) acc[nt][j][e] = 0.0f;
       }
-      p_low = past + row0 / p.group;
-      p_high = past + (row0 + rows - 1) / p.group;
+      p_low = past;
+      p_high = past + by_group(rem0 + rows - 1);
     }
     // N tiles of the warp together, W apart: their loads, products and exponentials overlap. Where the stage has
     // only some of them the others' weights are 0 (one path for all keeps the code in the instruction cache).
@@ -611,8 +624,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     if (flags & 2) {
       // The item's end: the warps join their parts, each in the place of its own tiles of this stage (four rows to a
       // tile), which is given back when all have read them.
-      auto part = [&](int w, int r) {
-        return reinterpret_cast<float*>(&sh.ring[s][((r >> 3) * WT + w + ((r >> 2) & 1) * W) * Sh::kTile]) + (r & 3) * D;
+      // (16-byte chunks of rows 2k and 2k + 1 are in the order c ^ k, which spreads a store over the banks)
+      auto part = [&](int w, int r, int d) {
+        return reinterpret_cast<float*>(&sh.ring[s][((r >> 3) * WT + w + ((r >> 2) & 1) * W) * Sh::kTile]) + (r & 3) * D +
+               (d ^ (((r >> 1) & 3) << 2));
       };
       float2(*stat)[R] = sh.stat[merges & 1];
       __syncwarp();
@@ -627,10 +642,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
           sum += __shfl_xor_sync(0xffffffffu, sum, 16);
           if (g == 0) stat[warp][r] = make_float2(m[nt][e], sum);
           if (r < rows) {
-            float* dst = part(warp, r) + D / 8 * g;
 #pragma unroll
             for (int j = 0; j < D / 16; ++j)
-              *reinterpret_cast<float2*>(dst + 2 * j) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
+              *reinterpret_cast<float2*>(part(warp, r, D / 8 * g + 2 * j)) = make_float2(acc[nt][j][e], acc[nt][j][e + 2]);
           }
         }
       __syncwarp();
@@ -647,7 +661,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
         for (int w = 0; w < W; ++w) {
           const float f = top == -INFINITY ? 0.0f : exp2_fast(stat[w][r].x - top);
-          const float4 x = *reinterpret_cast<const float4*>(part(w, r) + d);
+          const float4 x = *reinterpret_cast<const float4*>(part(w, r, d));
           sum = fmaf(f, stat[w][r].y, sum);
           o.x = fmaf(f, x.x, o.x);
           o.y = fmaf(f, x.y, o.y);
@@ -656,9 +670,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         }
         if (dest < 0) {
           const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
-          const int row = row0 + r;
-          uint16_t* dst = p.out + int64_t(t0 + row / p.group) * p.out_stride +
-                          int64_t(head * p.group + row % p.group) * D + d;
+          const int row = rem0 + r, tok = by_group(row);
+          uint16_t* dst = p.out + int64_t(t0 + tok) * p.out_stride + int64_t(head * p.group + row - tok * p.group) * D + d;
           *reinterpret_cast<uint2*>(dst) =
               make_uint2(Half16<T>::pack(o.x * inv, o.y * inv), Half16<T>::pack(o.z * inv, o.w * inv));
         } else {
@@ -935,6 +948,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   p.group = n_q_heads / cache->n_kv_heads;
   p.n_kv_heads = cache->n_kv_heads;
   p.whole = plan.whole;
+  p.inv_group = 1.0f / float(p.group);
   p.joins = static_cast<Join*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + size_t(plan.grid) * sizeof(Join));
 

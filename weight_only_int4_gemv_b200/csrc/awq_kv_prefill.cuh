@@ -37,7 +37,7 @@ constexpr int kSoftmaxWarps = 16, kWidenWarps = 4;
 constexpr int kPreThreads = (kSoftmaxWarps + kWidenWarps + 4) * 32;
 // What a segment costs beyond its tiles (q rows, first S, epilogue), in tiles: the schedule counts every item as
 // that much longer.
-constexpr int kSegmentCost = 2;
+constexpr int kSegmentCost = 3;
 constexpr float kLeastA = 7.888609052210118e-31f;    // 2^-100
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
