@@ -547,8 +547,8 @@ typedef struct awq_kv_rope {
  * where x are the (rotated) values in fp32 and s_old is the block's scale if
  * it holds earlier tokens of the sequence, else 0. If s > s_old their codes
  * c_old become round(c_old s_old / s). s is held in fp32 (top / R rounded
- * once); the quotients by it are rounded to nearest even exactly and clamped
- * to the codes' range. Appending the same rows at
+ * once); the quotients by it are rounded to nearest even exactly (E4M3: to
+ * fp32, then to the code) and clamped to the codes' range. Appending the same rows at
  * the same positions again leaves the same cache.
  * k, v [n_tokens][n_kv_heads][head_dim]. q [n_tokens][n_q_heads][head_dim]
  * and q_out (the same shape; may be q itself) are both given or both NULL;

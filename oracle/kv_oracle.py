@@ -33,8 +33,10 @@ def decode(codes: np.ndarray, fmt: str) -> np.ndarray:
 
 
 def encode(t: np.ndarray, fmt: str) -> np.ndarray:
-    """Nearest code of each value (ties to even), clamped."""
+    """Nearest code of each value (ties to even), clamped; e4m3 by way of fp32."""
     t = np.asarray(t, np.float64)
+    if fmt == "e4m3":
+        t = t.astype(np.float32).astype(np.float64)
     if fmt == "int8":
         return (np.clip(np.rint(t), -127, 127) + 128).astype(np.uint8)
     a = np.minimum(np.abs(t), 448.0)

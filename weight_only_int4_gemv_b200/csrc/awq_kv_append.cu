@@ -9,11 +9,12 @@
 //   c  = round(x / s),   R = 127 (int8) or 448 (e4m3)
 // with s_old only where the block holds earlier tokens of the sequence; if
 // that makes s grow, their codes become round(c_old s_old / s). x, maxima
-// and scales are fp32, and the quotients are rounded as the real numbers they
-// are: 16-bit values over the block's largest fall on the border between two
-// codes often enough (one in 10^4 or so) that a reciprocal's error would show
-// in the cache (0.0006 against 0.0002 of an e4m3 cache's values, in the
-// 2-norm), so a product that comes near a border is settled by its remainder.
+// and scales are fp32. The quotients are exact: for int8 codes rounded as the
+// real numbers they are, for e4m3 codes to fp32 and from there. 16-bit values
+// over the block's largest fall on the border between two codes often enough
+// (one in 10^4 or so) that a reciprocal's error would show in the cache
+// (0.0006 against 0.0002 of an e4m3 cache's values, in the 2-norm), so a
+// product that comes near a border is settled by a division.
 //
 // What bounds it: HBM bytes for prompts, launch and load latency for single
 // tokens. Hence one CTA per touched block of 16 tokens (so that a scale and
@@ -115,14 +116,17 @@ struct Turn {
   }
 };
 
-// x / s (x = hi + lo) rounded to odd in fp32: cut off, with the last bit set
-// where anything was cut, so that rounding it to a code rounds the quotient
-// itself. inv is 1 / s; the remainder fma(-q, s, hi) is exact.
-__device__ __forceinline__ float quotient_odd(float hi, float lo, float s, float inv) {
+// x / s (x = hi + lo), inv = 1 / s, ready to be rounded to a code. e4m3: to
+// the nearest fp32. int8: rounded to odd in fp32 (cut off, with the last bit
+// set where anything was cut), so that rounding it again rounds the quotient
+// itself. The remainder fma(-q, s, hi) is exact.
+template <int FMT>
+__device__ __forceinline__ float quotient(float hi, float lo, float s, float inv) {
   float q = hi * inv;
   if (q == 0.0f) return q;   // keeps its sign
   q = fmaf(fmaf(-q, s, hi), inv, q);
   const float r = fmaf(-q, s, hi) + lo;
+  if constexpr (FMT == AWQ_KV_E4M3) return fmaf(r, inv, q);
   uint32_t bits = __float_as_uint(q);
   if (r != 0.0f) bits = (bits - ((r < 0.0f) != (q < 0.0f) ? 1u : 0u)) | 1u;
   return __uint_as_float(bits);
@@ -131,7 +135,7 @@ __device__ __forceinline__ float quotient_odd(float hi, float lo, float s, float
 // The codes of eight values over the scale s (none above it by more than the
 // rounding of top / R). Products by inv give the quotients within 3 ulp; if
 // one of them comes that near to a border between two codes, all eight are
-// settled by their remainders.
+// divided.
 template <int FMT>
 __device__ __forceinline__ uint2 quantize8(const float (&x)[8], float s, float inv) {
   if constexpr (FMT == AWQ_KV_INT8) {
@@ -145,7 +149,7 @@ __device__ __forceinline__ uint2 quantize8(const float (&x)[8], float s, float i
     }
     if (far > 0.4999f) {   // 127 * 3 * 2^-24 < 10^-4
 #pragma unroll
-      for (int j = 0; j < 8; ++j) y[j] = rintf(quotient_odd(x[j], 0.0f, s, inv)) + kMagic;
+      for (int j = 0; j < 8; ++j) y[j] = rintf(quotient<FMT>(x[j], 0.0f, s, inv)) + kMagic;
     }
     uint32_t w[2];
 #pragma unroll
@@ -168,7 +172,7 @@ __device__ __forceinline__ uint2 quantize8(const float (&x)[8], float s, float i
     }
     if (near <= 16u || least < 0x3c7fffffu) {
 #pragma unroll
-      for (int j = 0; j < 8; ++j) t[j] = quotient_odd(x[j], 0.0f, s, inv);
+      for (int j = 0; j < 8; ++j) t[j] = __fdiv_rn(x[j], s);
     }
     return make_uint2(Code<FMT>::encode4(t), Code<FMT>::encode4(t + 4));
   }
@@ -276,7 +280,7 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
 #pragma unroll
         for (int j = 0; j < 8; ++j) {
           const float y = t[j] * old;
-          t[j] = quotient_odd(y, fmaf(t[j], old, -y), sc, inv);
+          t[j] = quotient<FMT>(y, fmaf(t[j], old, -y), sc, inv);
         }
         *dst = make_uint2(Code<FMT>::encode4(t), Code<FMT>::encode4(t + 4));
       }
