@@ -57,10 +57,14 @@ class Setup:
             dev.append(t[:, layers - 1])
         self.cache = awq.KvCache(dev[0], dev[1], dev[2], dev[3], fmt)
 
-    def batch(self, lens, new, max_q_len=None, table=None):
+    def batch(self, lens, new, max_q_len=None, table=None, wide=False):
+        """wide: room for long sequences in the table (its unused entries name no page), which with more than 64 rows
+        to a sequence and head makes the attention take its many-row kernel."""
         indptr = np.concatenate([[0], np.cumsum(new)])
-        return awq.KvBatch(torch.from_numpy(self.table if table is None else table).cuda(), i32(lens), i32(indptr),
-                           max_q_len)
+        table = self.table if table is None else table
+        if wide:
+            table = np.concatenate([table, np.full((len(table), 40000 // self.page), -1, np.int32)], 1)
+        return awq.KvBatch(torch.from_numpy(table).cuda(), i32(lens), i32(indptr), max_q_len)
 
     def poison(self, lens):
         """Blocks behind each sequence's last one get NaN scales and bytes; so do the bytes behind its end."""

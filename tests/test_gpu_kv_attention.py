@@ -17,13 +17,13 @@ def queries(rng, tokens, heads, dim, dtype, pad=0):
         x.as_strided((tokens, heads, dim), (heads * dim + pad, dim, 1))
 
 
-def run(s, lens, new, heads, dtype, window=0, sinks=0, scale=None, max_q_len=None, extra=0, pad=0, tag=""):
+def run(s, lens, new, heads, dtype, window=0, sinks=0, scale=None, max_q_len=None, extra=0, pad=0, tag="", wide=False):
     q = queries(s.rng, sum(new) + extra, heads, s.dim, dtype, pad)
     s.poison(lens)
     want, tol = s.expect(to64(q)[:sum(new)], lens, new, scale, window, sinks)
     out = torch.full(q.shape, 5.0, dtype=q.dtype, device="cuda")
-    got = awq.awq_kv_attention(q, s.cache, s.batch(lens, new, max_q_len), scale=scale, window=window, sinks=sinks,
-                               out=out)
+    got = awq.awq_kv_attention(q, s.cache, s.batch(lens, new, max_q_len, wide=wide), scale=scale, window=window,
+                               sinks=sinks, out=out)
     assert got is out
     assert awq.awq_device_error() == 0
     assert (out[sum(new):] == 5.0).all(), "rows behind the last sequence"
@@ -43,20 +43,22 @@ def test_single_tokens(dim, fmt, dtype, group):
 
 @pytest.mark.parametrize("dtype,fmt", [("fp16", "int8"), ("bf16", "e4m3")])
 @pytest.mark.parametrize("new", [[5, 0, 33, 64], [1, 2, 130, 7], [200, 1, 1, 16]])
-@pytest.mark.parametrize("dim,group", [(128, 4), (64, 1), (128, 7)])
-def test_several_tokens(dtype, fmt, new, dim, group):
+@pytest.mark.parametrize("dim,group", [(128, 4), (64, 1), (128, 7), (64, 16)])
+@pytest.mark.parametrize("wide", [False, True])
+def test_several_tokens(dtype, fmt, new, dim, group, wide):
     lens = [new[0], 90, 150, new[3] + 1]
     s = Setup(lens, 2, dim, 48, fmt, seed=sum(new))
-    run(s, lens, new, 2 * group, dtype, max_q_len=max(new), extra=1)
+    run(s, lens, new, 2 * group, dtype, max_q_len=max(new), extra=1, pad=8 * (group == 7), wide=wide)
 
 
 @pytest.mark.parametrize("window,sinks", [(1, 0), (1, 1), (16, 0), (16, 4), (17, 16), (40, 33), (7, 300), (1000, 4)])
 @pytest.mark.parametrize("new", [[1, 1, 1], [3, 40, 1], [150, 20, 9]])
 @pytest.mark.parametrize("dim,fmt", [(128, "int8"), (64, "e4m3")])
-def test_window_and_sinks(window, sinks, new, dim, fmt):
+@pytest.mark.parametrize("wide", [False, True])
+def test_window_and_sinks(window, sinks, new, dim, fmt, wide):
     lens = [250, 64, 9]
     s = Setup(lens, 2, dim, 16, fmt, seed=window + sinks)
-    run(s, lens, new, 6, "fp16", window=window, sinks=sinks)
+    run(s, lens, new, 6, "fp16", window=window, sinks=sinks, wide=wide)
 
 
 def test_rows_that_see_nothing():
@@ -64,8 +66,9 @@ def test_rows_that_see_nothing():
     lens, new = [0, 3, 0, 40, 5], [1, 5, 0, 2, 9]
     s = Setup([max(n, 1) for n in lens], 2, 128, 16, "int8", seed=11)
     for group in (1, 4, 40):
-        _, out = run(s, lens, new, 2 * group, "fp16")
-        assert (out[0] == 0).all() and (out[1:3] == 0).all()
+        for wide in (False, True):
+            _, out = run(s, lens, new, 2 * group, "fp16", wide=wide)
+            assert (out[0] == 0).all() and (out[1:3] == 0).all()
 
 
 @pytest.mark.parametrize("lens,heads,group", [([5000], 1, 4), ([3000, 1, 17, 2900], 2, 8), ([9000, 9001], 1, 1)])
@@ -73,6 +76,27 @@ def test_long_sequences_are_split(lens, heads, group):
     s = Setup(lens, heads, 128, 64, "int8", seed=12)
     run(s, lens, [1] * len(lens), heads * group, "fp16", max_q_len=1)
     run(s, lens, [min(3, n) for n in lens], heads * group, "bf16")
+
+
+@pytest.mark.parametrize("dtype,fmt,dim", [("fp16", "int8", 128), ("bf16", "e4m3", 64)])
+def test_many_rows_over_a_long_past_are_split(dtype, fmt, dim):
+    lens, new = [3000, 700, 140], [70, 33, 140]
+    s = Setup(lens, 1, dim, 64, fmt, seed=22)
+    run(s, lens, new, 3, dtype, wide=True)
+    run(s, lens, new, 3, dtype, window=300, sinks=130, wide=True)
+
+
+def test_many_rows_are_reproducible():
+    lens, new = [900, 260], [150, 260]
+    s = Setup(lens, 2, 128, 16, "int8", seed=23)
+    q = queries(s.rng, sum(new), 8, 128, "fp16")
+    batch = s.batch(lens, new, wide=True)
+    n = awq.awq_kv_attention_workspace_bytes(s.cache, batch, sum(new), 8)
+    first = awq.awq_kv_attention(q, s.cache, batch)
+    for fill in (0, 255):
+        ws = torch.full((n,), fill, dtype=torch.uint8, device="cuda")
+        for _ in range(3):
+            assert torch.equal(awq.awq_kv_attention(q, s.cache, batch, workspace=ws), first)
 
 
 def test_split_is_reproducible_and_workspace_free_of_state():
@@ -103,6 +127,7 @@ def test_scales_far_apart():
                  (s.cache.v_pages, s.ref.codes[1])):
         t.copy_(torch.from_numpy(a))
     run(s, lens, [20, 1], 8, "fp16")
+    run(s, lens, [40, 30], 8, "bf16", wide=True)
     run(s, lens, [1, 1], 2, "bf16", max_q_len=1)
 
 
@@ -110,6 +135,8 @@ def test_scales_far_apart():
 def test_other_logit_scales(scale):
     s = Setup([77, 31], 2, 64, 16, "int8", seed=15)
     run(s, [77, 31], [9, 31], 4, "fp16", scale=scale)
+    run(s, [77, 31], [70, 31], 4, "fp16", scale=scale, wide=True)
+    run(s, [77, 31], [70, 31], 4, "bf16", scale=scale, window=20, sinks=3, wide=True)
 
 
 def test_tiny_and_large_queries():
@@ -120,6 +147,10 @@ def test_tiny_and_large_queries():
         scale = 0.1 / size if size else 1.0
         want, tol = s.expect(to64(q), [50], [2], scale)
         check(awq.awq_kv_attention(q, s.cache, s.batch([50], [2]), scale=scale), want, tol, str(size))
+        # the many-row kernel, rows that see nothing among them
+        q = (queries(s.rng, 45, 4, 128, "bf16").double() * size).to(torch.bfloat16)
+        want, tol = s.expect(to64(q), [40], [45], scale)
+        check(awq.awq_kv_attention(q, s.cache, s.batch([40], [45], wide=True), scale=scale), want, tol, str(size))
 
 
 def test_shared_pages_and_many_sequences():
@@ -148,6 +179,15 @@ def test_bad_pages_are_recorded():
     want, tol = s.expect(to64(q), [100, 40], [1, 1])
     check(out[1:], want[1:], tol[1:], "the other sequence")
     awq.awq_kv_attention(q, s.cache, awq.KvBatch(torch.from_numpy(s.table).cuda(), i32([2 ** 30, -4]), i32([0, 5, 3])))
+    assert awq.awq_device_error() == 16
+    # the many-row kernel
+    q = queries(s.rng, 70, 8, 128, "fp16")
+    out = awq.awq_kv_attention(q, s.cache, s.batch([100, 40], [40, 30], table=table, wide=True))
+    assert awq.awq_device_error() == 16
+    want, tol = s.expect(to64(q), [100, 40], [40, 30])
+    check(out[40:], want[40:], tol[40:], "the other sequence")
+    bad = s.batch([100, 40], [40, 30], wide=True)
+    awq.awq_kv_attention(q, s.cache, awq.KvBatch(bad.block_table, i32([2 ** 30, -4]), i32([-3, 200, 50])))
     assert awq.awq_device_error() == 16
 
 

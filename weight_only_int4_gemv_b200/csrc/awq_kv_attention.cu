@@ -766,7 +766,7 @@ __global__ void __launch_bounds__(kJoinThreads) join_kernel(const __grid_constan
 using DecodeFn = void (*)(CUtensorMap, CUtensorMap, AttentionParams);
 using JoinFn = void (*)(AttentionParams);
 
-// kind 0, 1: up to 8 / 16 rows a tile; 2: pairs of row tiles of 128.
+// kind 0, 1: tiles of 8 / 16 rows; 2: pairs of row tiles of 128.
 struct Variant {
   DecodeFn main;
   JoinFn join;
@@ -825,9 +825,14 @@ size_t workspace_of(const Variant& v, int grid, int d) {
   return size_t(grid) * sizeof(Join) + size_t(grid) * 2 * v.R * (d + 2) * sizeof(float);
 }
 
-// By the rows (tokens x group) of the longest sequence: tiles of 8 while they
-// fit one, of 16 while they fit that, else pairs of 128.
-int kind_of(int64_t rows) { return rows <= 8 ? 0 : rows <= 16 ? 1 : 2; }
+// The kernel, by the rows (tokens x group) of the longest sequence and the (rows of the call) x (tiles of 16 keys that
+// fit a sequence): tiles of 8 rows while they fit one; beyond, tiles of 16, which read the cache once each but start
+// fast and share the work finely, until the pairs of 128 on the tensor cores win. Measured (32 / 8 heads of 128, int8;
+// tiles of 16 and pairs of 128, us):
+//   16 sequences of 2000 tokens, 48 and 96 rows each:       35 and 51, 54 and 51
+//   1 sequence, 240 rows, 60, 2000, 8000 tokens:            7 and 16, 24 and 30, 58 and 43
+//   1 sequence, 480 rows, 120, 2000 tokens:                 9 and 16, 38 and 30
+int kind_of(int64_t rows, int64_t all, int64_t tiles) { return rows <= 8 ? 0 : rows <= 64 || all * tiles <= 32768 ? 1 : 2; }
 
 awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
                              int32_t n_q_heads) {
@@ -857,7 +862,8 @@ awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, i
                      int32_t n_q_heads, Plan* plan) {
   const int group = n_q_heads / cache->n_kv_heads;
   const int64_t most = batch->max_q_len > 0 && batch->max_q_len < n_tokens ? batch->max_q_len : n_tokens;
-  const int kind = kind_of(most * group);
+  const int64_t tiles = int64_t(batch->max_pages) * (cache->page_size / kBlock) + 1;   // of the longest sequence that fits
+  const int kind = kind_of(most * group, n_tokens * group, tiles);
   plan->v = dtype == AWQ_KV_FP16 ? variant_of<__half>(cache->head_dim, cache->format, kind)
                                  : variant_of<__nv_bfloat16>(cache->head_dim, cache->format, kind);
   plan->many = kind == 2;
@@ -865,7 +871,6 @@ awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, i
   const awq_status_t st = resident(plan->v, key, &plan->grid);
   if (st != AWQ_OK) return st;
   // No more CTAs than the longest sequences that fit could give work to.
-  const int64_t tiles = int64_t(batch->max_pages) * (cache->page_size / kBlock) + 1;
   const int64_t work = plan->many ? (tiles + 7) / 8 * ((n_tokens * group + kPairRows - 1) / kPairRows + batch->n_seqs)
                                   : (tiles + WT - 1) / WT * ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs);
   const int64_t items = ((n_tokens * group + plan->v.R - 1) / plan->v.R + batch->n_seqs) * cache->n_kv_heads;
