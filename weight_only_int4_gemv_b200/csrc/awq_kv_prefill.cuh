@@ -30,13 +30,21 @@
 //
 // Work is laid end to end in units of 128 keys and cut evenly over the CTAs,
 // as for few rows; split items meet in join_rows_kernel.
+//
+// Measured on one B200: chunks of up to 509 rows x 8 heads over up to 6001
+// tokens, 8 key / value heads of 128, e4m3: 226 us, 676 TFLOP/s (39 % of a
+// dense bf16 product's measured rate); a prompt of 2048, 32 / 8 heads, int8: 72
+// us, 475 TFLOP/s; 4096 with a window of 1024: 135 us, 447. Two thirds of the
+// tensor pipe's cycles are idle: S -> softmax -> P -> next S is a chain of
+// latencies (softmax 2800 to 3900 cycles, both products 2000) with two row
+// tiles in flight, and tensor memory has no room for a third.
 
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
 constexpr int kSoftmaxWarps = 16, kWidenWarps = 4;
 constexpr int kPreThreads = (kSoftmaxWarps + kWidenWarps + 4) * 32;
 // What a segment costs beyond its tiles (q rows, first S, epilogue), in tiles: the schedule counts every item as
-// that much longer.
+// that much longer (1, 2, 3, 4: chunks of 509 rows over 6000 295, 254, 226, 226 us; a prompt of 2048 81, 72, 72, 73).
 constexpr int kSegmentCost = 3;
 constexpr float kLeastA = 7.888609052210118e-31f;    // 2^-100
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
@@ -97,17 +105,13 @@ __device__ __forceinline__ void tc_mma_ts(uint32_t d, uint32_t a, uint64_t b, ui
       "r"(accumulate)
       : "memory");
 }
-// One lane of a converged warp. The tensor core's instructions take uniform
-// operands: behind this predicate the compiler issues them as they are,
-// behind `lane == 0` it wraps each one (about 150 cycles instead of 64 for a
-// 128 x 128 x 16 product).
+// One lane of a converged warp.
 __device__ __forceinline__ bool elect_one() {
   uint32_t p;
   asm volatile("{\n\t.reg .pred p;\n\telect.sync _|p, 0xffffffff;\n\tselp.u32 %0, 1, 0, p;\n\t}" : "=r"(p));
   return p != 0;
 }
-// this warp's 32 lanes x 32 columns. The wait is in the same statement: nothing may read r before it, and as a
-// statement of its own with r as operands it costs a register move each.
+// this warp's 32 lanes x 32 columns. The wait is in the same statement: nothing may read r before it.
 __device__ __forceinline__ void tc_ld16(uint32_t a, uint32_t (&r)[16]) {
   asm volatile(
       "tcgen05.ld.sync.aligned.32x32b.x16.b32 "
