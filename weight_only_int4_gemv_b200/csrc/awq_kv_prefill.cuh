@@ -257,6 +257,9 @@ __device__ __forceinline__ void widen16(const uint4& c, uint4& a, uint4& b) {
   b = make_uint4(code_pair<FMT, 0>(c.z), code_pair<FMT, 2>(c.z), code_pair<FMT, 0>(c.w), code_pair<FMT, 2>(c.w));
 }
 
+// The lowest n bits.
+__device__ __forceinline__ uint32_t low_bits(int n) { return n >= 32 ? 0xffffffffu : n <= 0 ? 0u : (1u << n) - 1u; }
+
 // Largest (smallest) of 16.
 template <class Op3>
 __device__ __forceinline__ float extreme16(const uint32_t* r, Op3 op) {
@@ -368,12 +371,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           // masked columns of S become the infinity that a's sign takes to -inf
 #pragma unroll 1
           for (int c = 0; c < kTile / 64; ++c) {
+            const uint32_t vis = low_bits(hi - 32 * c + 1) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+            if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
             uint32_t r[32];
             tc_ld32(ts + c * 32, r);
-            const int h = hi - 32 * c, lw = lo - 32 * c, s = sk - 32 * c;
 #pragma unroll
             for (int k = 0; k < 32; ++k)
-              if (!((k <= h) & ((k >= lw) | (k < s)))) r[k] = flip ? 0x7f800000u : 0xff800000u;
+              if (!(vis & (1u << k))) r[k] = flip ? 0x7f800000u : 0xff800000u;
             tc_st32(ts + c * 32, r);
           }
           tc_wait_st();
