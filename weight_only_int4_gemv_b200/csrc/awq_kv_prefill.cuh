@@ -278,7 +278,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   extern __shared__ uint8_t smem_raw[];
   // (an offset from the array, not a rounded address: the compiler then knows it is shared memory)
   Sh& sh = *reinterpret_cast<Sh*>(smem_raw + ((0u - smem_u32(smem_raw)) & 1023u));
-  const int warp = threadIdx.x >> 5, lane = threadIdx.x & 31;
+  // The warps' parts by number (a scheduler has every fourth warp): 16, 18, 19, 20 widen, so that the products' warp,
+  // 17, shares its scheduler with no widening one; 21 and 23 bring q, 22 the schedule.
+  const int lane = threadIdx.x & 31, hw_warp = threadIdx.x >> 5;
+  const int warp = hw_warp < 17 ? hw_warp : hw_warp == 17 ? 21 : hw_warp < 21 ? hw_warp - 1 : hw_warp == 21 ? 22 : hw_warp == 22 ? 20 : 23;
   volatile int* abort = &sh.abort;
   uint32_t* err = &g_kv_attention_error;
   if (threadIdx.x == 0) {
@@ -529,7 +532,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     // A thread takes 16-byte chunk k of the rows r0, r0 + kRowStep, ...: 16 channels, chunks 2k and 2k + 1 (mod 8) of
     // its panel's row. Eight lanes read eight chunks at once, and write to eight different ones: with two panels,
     // lanes 4-7 take the row beside lanes 0-3's, whose chunks the swizzle puts on the other places.
-    const int tid = threadIdx.x - kSoftmaxWarps * 32;
+    const int tid = (warp - kSoftmaxWarps) * 32 + lane;
     constexpr int CPR = D / 16, kRowStep = 128 / CPR;
     const int k = tid % CPR, r0 = D == 128 ? (tid >> 3) ^ (k >> 2) : tid / CPR;
     const int raw_at = r0 * D + k * 16, half_at = (k >> 2) * (kTile * 128) + r0 * 128;
