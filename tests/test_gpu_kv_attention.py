@@ -273,3 +273,15 @@ def test_two_streams_at_once():
     for i in range(2):
         for y in got[i]:
             assert torch.equal(y, want[i])
+
+
+def test_many_short_prompts():
+    """More sequences than a warp has lanes, of more than 64 rows each, among them empty ones and one of many tiles of
+    rows: the many-row kernel's schedule."""
+    rng = np.random.default_rng(23)
+    new = [int(n) for n in rng.integers(0, 20, 75)]
+    new[3], new[40], new[41], new[74] = 700, 0, 19, 18
+    lens = [n + int(e) for n, e in zip(new, rng.integers(-3, 60, 75))]
+    lens = [max(n, 0) for n in lens]
+    s = Setup(lens, 1, 64, 16, "int8", seed=24)
+    run(s, lens, new, 4, "fp16", wide=True)

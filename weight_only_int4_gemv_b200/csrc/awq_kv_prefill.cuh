@@ -240,14 +240,36 @@ __device__ __forceinline__ Pair pair_of(const AttentionParams& p, const Seq& s, 
   return r;
 }
 
-// Units of a sequence (all lanes of a warp together).
-__device__ __forceinline__ int64_t pair_units(const AttentionParams& p, const Seq& s, int lane) {
-  const int pairs = (s.n * p.group + kPairRows - 1) / kPairRows;
-  int64_t sum = 0;
-  for (int i = lane; i < pairs; i += 32) sum += pair_of(p, s, i * kPairRows).tiles + kSegmentCost;
+// Units of 32 sequences, one to a lane: a lane counts a short one by itself, the warp the long ones in turn. (133
+// sequences of up to 96 rows over 278 tokens, all in turn and like this: 125 and 31 us; 600 of up to 96 over 42: 484
+// and 52.)
+__device__ __forceinline__ int64_t units_of(const AttentionParams& p, const Seq& mine, int lane) {
+  constexpr int kShort = 8;
+  const int all = (mine.n * p.group + kPairRows - 1) / kPairRows;
+  unsigned left = __ballot_sync(0xffffffffu, all > kShort);
+  Seq s = mine;
+  int first = 0, step = 1, pairs = all > kShort ? 0 : all;
+  int64_t units = 0;
+#pragma unroll 1
+  for (int who = lane;;) {
+    int64_t sum = 0;
+#pragma unroll 1
+    for (int i = first; i < pairs; i += step) sum += pair_of(p, s, i * kPairRows).tiles + kSegmentCost;
+    if (step > 1) {
 #pragma unroll
-  for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
-  return sum * p.n_kv_heads;
+      for (int o = 16; o > 0; o >>= 1) sum += __shfl_xor_sync(0xffffffffu, sum, o);
+    }
+    if (who == lane) units += sum;
+    if (!left) break;
+    who = __ffs(left) - 1;
+    left &= left - 1;
+    first = lane;
+    step = 32;
+    s = {__shfl_sync(0xffffffffu, mine.t0, who), __shfl_sync(0xffffffffu, mine.n, who),
+         __shfl_sync(0xffffffffu, mine.len, who), __shfl_sync(0xffffffffu, mine.past, who)};
+    pairs = __shfl_sync(0xffffffffu, all, who);
+  }
+  return units * p.n_kv_heads;
 }
 
 // 16 raw codes to 16 fp16 numbers, two 16-byte chunks.
@@ -583,35 +605,53 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     }
   } else if (warp == kSoftmaxWarps + kWidenWarps) {
     // --------------------------------------------- the schedule, pages, copies
-    int64_t total = 0;
     const Batch& a = p.batch;
-    for (int b0 = 0; b0 < a.n_seqs; b0 += 32) {
-      Seq mine = {0, 0, 0, 0};
-      if (b0 + lane < a.n_seqs) mine = load_seq(a, b0 + lane, err);
-      for (int i = 0; i < min(32, a.n_seqs - b0); ++i) {
-        const Seq s = {__shfl_sync(0xffffffffu, mine.t0, i), __shfl_sync(0xffffffffu, mine.n, i),
-                       __shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.past, i)};
-        total += pair_units(p, s, lane);
-      }
-    }
-    const int64_t per = (total + gridDim.x - 1) / gridDim.x;
-    const int64_t u0 = per * blockIdx.x, u1 = min(u0 + per, total);
     Join join;
     join.last = -1;
     int it = 0, n = 0;
     bool ok = true;
+    // The first walk over the sequences counts the units, the second one hands out this CTA's.
+    int64_t total = 0, per = 0, u0 = 0, u1 = 0;
     int64_t u = 0;                               // units before the sequence
-    for (int b0 = 0; b0 < a.n_seqs && u < u1 && ok; b0 += 32) {
+    bool counting = true;
+#pragma unroll 1
+    for (int b0 = 0; ok; b0 += 32) {
+      if (b0 >= a.n_seqs) {
+        if (!counting) break;
+        counting = false;
+#pragma unroll
+        for (int o = 16; o > 0; o >>= 1) total += __shfl_xor_sync(0xffffffffu, total, o);
+        per = divide(total + gridDim.x - 1, gridDim.x);
+        u0 = per * blockIdx.x;
+        u1 = min(u0 + per, total);
+        b0 = -32;
+        continue;
+      }
+      if (!counting && u >= u1) break;
       Seq mine = {0, 0, 0, 0};
       if (b0 + lane < a.n_seqs) mine = load_seq(a, b0 + lane, err);
-      for (int i = 0; i < min(32, a.n_seqs - b0) && u < u1 && ok; ++i) {
+      const int64_t own_units = units_of(p, mine, lane);
+      if (counting) {
+        total += own_units;
+        continue;
+      }
+      int64_t before = own_units;
+#pragma unroll
+      for (int o = 1; o < 32; o <<= 1) {
+        const int64_t y = __shfl_up_sync(0xffffffffu, before, o);
+        if (lane >= o) before += y;
+      }
+      const unsigned reach = __ballot_sync(0xffffffffu, u + before > u0);
+      if (!reach) {
+        u += __shfl_sync(0xffffffffu, before, 31);
+        continue;
+      }
+      const int i0 = __ffs(reach) - 1;           // the first sequence with units of this run
+      u += __shfl_sync(0xffffffffu, before - own_units, i0);
+      for (int i = i0; i < min(32, a.n_seqs - b0) && u < u1 && ok; ++i) {
         const Seq s = {__shfl_sync(0xffffffffu, mine.t0, i), __shfl_sync(0xffffffffu, mine.n, i),
                        __shfl_sync(0xffffffffu, mine.len, i), __shfl_sync(0xffffffffu, mine.past, i)};
-        const int64_t units = pair_units(p, s, lane);
-        if (u + units <= u0) {
-          u += units;
-          continue;
-        }
+        const int64_t units = __shfl_sync(0xffffffffu, own_units, i);
         const int32_t* table = a.table + int64_t(b0 + i) * a.table_stride;
         const int rows = s.n * p.group, pairs = (rows + kPairRows - 1) / kPairRows;
         int64_t begin = u;                       // units before the pair
