@@ -467,8 +467,8 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
  * pages page_stride bytes and scale_stride floats apart (the rest is dense),
  * so a layer's pages may be a slice of a larger array. A held value is
  *   AWQ_KV_INT8: s * (code - 128), codes 1 .. 255
- *   AWQ_KV_E4M3: s * e4m3(code); the codes 0x7f and 0xff (NaN) are never
- *                written, and attention over them is unspecified
+ *   AWQ_KV_E4M3: s * e4m3(code); the codes 0x7f and 0xff (NaN) are not written
+ *                for finite values, and attention over them is unspecified
  * head_dim is 64 or 128; page_size a multiple of 16, up to 65536.
  *
  * A batch says which tokens a call is about. Sequence b holds seq_lens[b]
@@ -549,8 +549,11 @@ typedef struct awq_kv_rope {
  * it holds earlier tokens of the sequence, else 0. If s > s_old their codes
  * c_old become round(c_old s_old / s). s is held in fp32 (top / R rounded
  * once); the quotients by it are rounded to nearest even exactly (E4M3: to
- * fp32, then to the code) and clamped to the codes' range. Appending the same rows at
- * the same positions again leaves the same cache.
+ * fp32, then to the code) and clamped to the codes' range. Appending the same
+ * rows at the same positions again leaves the same cache. A NaN or an infinity
+ * among x makes s, and what is read from the block's head, NaN or infinite
+ * until the block is written again from its first token; other blocks and
+ * heads, and attention rows that do not see the block, are as without it.
  * k, v [n_tokens][n_kv_heads][head_dim]. q [n_tokens][n_q_heads][head_dim]
  * and q_out (the same shape; may be q itself) are both given or both NULL;
  * q_out = q turned, rounded once. rope NULL: nothing is turned. Only the

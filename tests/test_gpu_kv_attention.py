@@ -275,6 +275,34 @@ def test_two_streams_at_once():
             assert torch.equal(y, want[i])
 
 
+@pytest.mark.parametrize("wide", [False, True])
+@pytest.mark.parametrize("which", ["k_scales", "v_scales"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf")])
+@pytest.mark.parametrize("dtype,fmt", [("fp16", "int8"), ("bf16", "e4m3")])
+def test_a_spoilt_block_stays_with_the_rows_that_see_it(dtype, fmt, value, which, wide):
+    """A block whose scale is not finite, in the same tiles as rows that do not see it: because they come before it,
+    because the window has left it, because they belong to another head."""
+    new = [45, 50] if wide else [10, 8]
+    lens = [300, 84]                         # block 5 (positions 80 .. 95) is spoilt
+    window, heads = 200, 8
+    s = Setup(lens, 2, 128, 16, fmt, seed=22)
+    for b in range(2):
+        getattr(s.cache, which)[int(s.table[b, 5]), 0] = value
+    q = queries(s.rng, sum(new), heads, 128, dtype)
+    want, tol = s.expect(to64(q), lens, new, window=window)
+    got = awq.awq_kv_attention(q, s.cache, s.batch(lens, new, wide=wide), window=window)
+    assert awq.awq_device_error() == 0
+    p = np.concatenate([np.arange(n - a, n) for n, a in zip(lens, new)])
+    sees = (p >= 80) & (p - window < 95)
+    assert sees.any() and not sees.all()
+    half = heads // 2
+    check(got[:, half:], want[:, half:], tol[:, half:], "the other head")
+    clean = np.flatnonzero(~sees)
+    check(got[torch.from_numpy(clean).cuda(), :half], want[clean, :half], tol[clean, :half], "rows that do not see it")
+    if value != value:
+        assert not torch.isfinite(got[torch.from_numpy(np.flatnonzero(sees)).cuda(), :half]).any()
+
+
 def test_many_short_prompts():
     """More sequences than a warp has lanes, of more than 64 rows each, among them empty ones and one of many tiles of
     rows: the many-row kernel's schedule."""

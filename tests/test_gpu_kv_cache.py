@@ -215,3 +215,36 @@ def test_many_sequences():
                 s.ref.append(w, s.table[b], lens[b] - 1, to64(x[w, at:at + 1]))
             at += 1
     check_cache(s, [np.zeros(c.shape) for c in s.ref.codes], True, "many")
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", ["fp16", "bf16"])
+def test_non_finite_rows_spoil_their_block_alone(fmt, dtype):
+    """A NaN or an infinity shows in its block's scale, leaves the other blocks and heads as they would be, and is gone
+    when the block is written again from its first token."""
+    s = Setup([100], 2, 64, 16, fmt, seed=9)
+    batch = s.batch([100], [100])
+    tensors = (s.cache.k_pages, s.cache.v_pages, s.cache.k_scales, s.cache.v_scales)
+    rows = torch.from_numpy(s.rng.standard_normal((2, 100, 2, 64))).cuda().to(DT[dtype])
+    awq.awq_kv_append(rows[0], rows[1], s.cache, batch)
+    clean = [t.clone() for t in tensors]
+    bad = rows.clone()
+    spoilt = [(0, 20, 0, float("nan")), (0, 99, 1, float("-inf")), (1, 40, 1, float("inf")), (1, 64, 0, float("nan"))]
+    for w, token, head, value in spoilt:
+        bad[w, token, head, 7 * (token % 9)] = value
+    awq.awq_kv_append(bad[0], bad[1], s.cache, batch)
+    for w in range(2):
+        keep = torch.ones(clean[2 + w].shape, dtype=torch.bool, device="cuda")
+        for _, token, head, _ in (e for e in spoilt if e[0] == w):
+            at = int(s.table[0, token // 16]), head, 0
+            assert not torch.isfinite(tensors[2 + w][at]), (w, token)
+            keep[at] = False
+        assert torch.equal(tensors[2 + w][keep], clean[2 + w][keep])
+        codes = [t[w].view(t[w].shape[0], 2, 1, 16, 64) for t in (tensors, clean)]
+        assert torch.equal(codes[0][keep], codes[1][keep])
+    held = awq.awq_kv_dequant(s.cache, batch, 100, DT[dtype])
+    for w, token, head, value in spoilt:
+        assert not torch.isfinite(held[w][token, head, 7 * (token % 9)]), (w, token)
+    awq.awq_kv_append(rows[0], rows[1], s.cache, batch)
+    for a, b in zip(tensors, clean):
+        assert torch.equal(a, b)

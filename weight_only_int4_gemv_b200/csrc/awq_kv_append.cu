@@ -61,6 +61,13 @@ __device__ __forceinline__ int touched(const Seq& s) {
   return s.len > p0 ? (s.len - 1) / kBlock - p0 / kBlock + 1 : 0;
 }
 
+// max(a, |x|, |y|), NaN if one of them is: a block with a NaN gets that as its scale and does not look sound.
+__device__ __forceinline__ float max_abs_nan(float a, float x, float y) {
+  float r;
+  asm("max.NaN.abs.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(x), "f"(y));
+  return r;
+}
+
 __device__ __forceinline__ void load4(const float* p, float* v) {
   const float4 f = *reinterpret_cast<const float4*>(p);
   v[0] = f.x;
@@ -258,16 +265,16 @@ __global__ void __launch_bounds__(kThreads, 3) append_kernel(const __grid_consta
         turn.apply(x[i]);
       }
 #pragma unroll
-      for (int j = 0; j < 8; ++j) top = fmaxf(top, fabsf(x[i][j]));
+      for (int j = 0; j < 8; j += 2) top = max_abs_nan(top, x[i][j], x[i][j + 1]);
     }
     if (task + teams < tasks) fetch(task + teams);
 #pragma unroll
-    for (int o = 16; o > 0; o >>= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, o));
+    for (int o = 16; o > 0; o >>= 1) top = max_abs_nan(top, __shfl_xor_sync(0xffffffffu, top, o), 0.0f);
     if (lane == 0) tops[round][warp] = top;
     // (both warps have read the old scale, too)
     asm volatile("bar.sync %0, 64;" ::"r"(1 + (warp >> 1)) : "memory");
-    top = fmaxf(top, tops[round][warp ^ 1]);
-    const float sc = fmaxf(fmaxf(__fdiv_rn(top, Code<FMT>::kTop), old), kScaleFloor);
+    top = max_abs_nan(top, tops[round][warp ^ 1], 0.0f);
+    const float sc = max_abs_nan(__fdiv_rn(top, Code<FMT>::kTop), old, kScaleFloor);
     const float inv = __fdiv_rn(1.0f, sc);
 #pragma unroll
     for (int i = 0; i < PASSES; ++i) {

@@ -506,7 +506,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         ks[u] = tile[u] < 0 ? 0.0f : me.ks[i];
         const float vs = tile[u] < 0 ? 1.0f : me.vs[i];
         lv[u] = __log2f(vs);
-        iv[u] = __fdividef(1.0f / kShift<FMT>, vs);   // (O holds codes / kShift)
+        // (O holds codes / kShift; a scale that is no positive number must not reach the rows that do not see its block)
+        iv[u] = vs > 0.0f ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;
       }
       // S = K q^T
       float sc[N][NT][4];

@@ -47,6 +47,7 @@ constexpr int kPreThreads = (kSoftmaxWarps + kWidenWarps + 4) * 32;
 // that much longer (1, 2, 3, 4: chunks of 509 rows over 6000 295, 254, 226, 226 us; a prompt of 2048 81, 72, 72, 73).
 constexpr int kSegmentCost = 3;
 constexpr float kLeastA = 7.888609052210118e-31f;    // 2^-100
+constexpr float kSpoilt = 3.4028234663852886e38f;    // the largest number: no logit's size
 constexpr int kRawSlots = 3, kHalfSlots = 3, kMetaSlots = 4;
 
 enum : int {                                   // PreMeta::flags
@@ -58,7 +59,12 @@ enum : int {                                   // PreMeta::flags
   kStop = 1024                                 // no more tiles
 };
 
-struct PreMeta {
+// 1 / l; 0 for a row that sees nothing, NaN for one that sees a block without a finite scale.
+__device__ __forceinline__ float inverse(float m, float l) {
+  return m == -INFINITY ? 0.0f : m >= kSpoilt ? __uint_as_float(0x7fffffffu) : __fdiv_rn(1.0f, l);
+}
+
+struct alignas(16) PreMeta {     // (its arrays are read two floats at a time)
   int pos, flags;
   int t0, row0, rows, past, head, dest;
   float ks[8], vs[8];            // the blocks' scales
@@ -503,7 +509,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           both_ph ^= 1;
           l += sh.mass[x][half ^ 1][row];
         }
-        const float inv = m == -INFINITY ? 0.0f : __fdiv_rn(1.0f, l);
+        const float inv = inverse(m, l);
 #pragma unroll 1
         for (int c = 0; c < D / 64; ++c) {
           uint32_t r[32];
@@ -568,10 +574,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       if (flags & kStop) break;
       if (tid < 8) {                             // (published with the keys)
         PreMeta& out = sh.meta[mi];
-        const float a = fmaxf(fabsf(p.scale_log2) * kShift<FMT> * me.ks[tid], kLeastA);
+        // A scale that is not finite must not reach the rows that do not see its block (there t is -inf by S, whatever
+        // finite numbers stand here) and has to show in the others: their m becomes kSpoilt, which ends as NaN.
+        const float ks = me.ks[tid], vs = me.vs[tid];
+        const bool fine = ks - ks == 0.0f && vs - vs == 0.0f && vs > 0.0f;
+        const float a = fine ? fmaxf(fabsf(p.scale_log2) * kShift<FMT> * ks, kLeastA) : kLeastA;
         out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
-        out.lv[tid] = __log2f(me.vs[tid]);
-        out.iv[tid] = __fdividef(1.0f / kShift<FMT>, me.vs[tid]);   // (O holds codes / kShift)
+        out.lv[tid] = fine ? __log2f(vs) : kSpoilt;
+        out.iv[tid] = fine ? __fdividef(1.0f / kShift<FMT>, vs) : 1.0f;   // (O holds codes / kShift)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
@@ -1026,7 +1036,7 @@ __global__ void __launch_bounds__(256) join_rows_kernel(const __grid_constant__ 
       o[e].w = fmaf(f, y.w, o[e].w);
     }
   }
-  const float inv = top == -INFINITY ? 0.0f : __fdiv_rn(1.0f, sum);
+  const float inv = inverse(top, sum);
 #pragma unroll
   for (int e = 0; e < D / 32; ++e)
     *reinterpret_cast<uint2*>(tile + lane * kRow + (e * 8 + warp) * 8) =
