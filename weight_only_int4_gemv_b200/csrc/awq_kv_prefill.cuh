@@ -32,12 +32,14 @@
 // as for few rows; split items meet in join_rows_kernel.
 //
 // Measured on one B200: chunks of up to 509 rows x 8 heads over up to 6001
-// tokens, 8 key / value heads of 128, e4m3: 226 us, 676 TFLOP/s (39 % of a
-// dense bf16 product's measured rate); a prompt of 2048, 32 / 8 heads, int8: 72
-// us, 475 TFLOP/s; 4096 with a window of 1024: 135 us, 447. Two thirds of the
+// tokens, 8 key / value heads of 128, e4m3: 224 us, 681 TFLOP/s (40 % of a
+// dense bf16 product's measured rate); a prompt of 2048, 32 / 8 heads, int8: 69
+// us, 494 TFLOP/s; 4096 with a window of 1024: 125 us, 483. Two thirds of the
 // tensor pipe's cycles are idle: S -> softmax -> P -> next S is a chain of
 // latencies (softmax 2800 to 3900 cycles, both products 2000) with two row
-// tiles in flight, and tensor memory has no room for a third.
+// tiles in flight, and tensor memory has no room for a third. The exponential
+// unit is not the bound: every fourth (third, second) pair of exponentials as
+// a polynomial on the FMA pipe took 71 (71, 74) us for the prompt.
 
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
