@@ -313,3 +313,29 @@ def test_many_short_prompts():
     lens = [max(n, 0) for n in lens]
     s = Setup(lens, 1, 64, 16, "int8", seed=24)
     run(s, lens, new, 4, "fp16", wide=True)
+
+
+def test_two_graphs_share_a_workspace():
+    """A chunk of prompt (many-row kernel) and single tokens (split over CTAs), captured apart, with one workspace,
+    replayed in turn."""
+    lens = [900, 700]
+    s = Setup(lens, 2, 128, 16, "int8", seed=25)
+    calls = [(s.batch(lens, [150, 90], wide=True), queries(s.rng, 240, 8, 128, "bf16")),
+             (s.batch(lens, [1, 1], 1), queries(s.rng, 2, 8, 128, "bf16"))]
+    want = [awq.awq_kv_attention(q, s.cache, b) for b, q in calls]
+    n = max(awq.awq_kv_attention_workspace_bytes(s.cache, b, q.shape[0], 8) for b, q in calls)
+    ws = torch.empty(n, dtype=torch.uint8, device="cuda")
+    outs, graphs = [torch.zeros_like(y) for y in want], []
+    for (b, q), out in zip(calls, outs):
+        graph = torch.cuda.CUDAGraph()
+        with torch.cuda.graph(graph):
+            awq.awq_kv_attention(q, s.cache, b, out=out, workspace=ws)
+        graphs.append(graph)
+    for order in ((0, 1), (1, 0), (0, 0), (1, 1)):
+        for out in outs:
+            out.fill_(7.0)
+        for i in order:
+            graphs[i].replay()
+        for i in set(order):
+            assert torch.equal(outs[i], want[i])
+    assert awq.awq_device_error() == 0
