@@ -109,11 +109,12 @@ class Cache:
         return quotients
 
 
-def attention(q, k, v, past, scale, window=0, sinks=0, top=None):
+def attention(q, k, v, past, scale, window=0, sinks=0, top=None, keep=None):
     """q [rows, heads, dim] at positions past .., k, v [len, kv_heads, dim]:
     (out, sum of weight * |v|, largest scale * sum |q| |k|, keys seen times the
     largest weight * top), the first two [rows, heads, dim], the others
-    [rows, heads]. top [len, kv_heads]."""
+    [rows, heads]. top [len, kv_heads]. keep [len]: keys that are there (None:
+    all)."""
     rows, heads, dim = q.shape
     n, kv = k.shape[:2]
     group = heads // kv
@@ -125,6 +126,8 @@ def attention(q, k, v, past, scale, window=0, sinks=0, top=None):
         see = j <= p
         if window:
             see &= (j > p - window) | (j < sinks)
+        if keep is not None:
+            see &= keep
         if not see.any():
             continue
         for h in range(heads):

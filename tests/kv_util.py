@@ -79,15 +79,17 @@ class Setup:
                     if off // 16 * 16 >= n - pos + off:
                         scales[pg, :, off // 16] = float("nan")
 
-    def expect(self, q, lens, new, scale=None, window=0, sinks=0):
-        """Oracle outputs and the elementwise tolerance for q [tokens, heads, dim] (float64)."""
+    def expect(self, q, lens, new, scale=None, window=0, sinks=0, keep=None):
+        """Oracle outputs and the elementwise tolerance for q [tokens, heads, dim] (float64). keep: for each sequence
+        which of its keys are there (None: all)."""
         scale = self.dim ** -0.5 if scale is None else scale
         out, tol, at = np.zeros_like(q), np.zeros_like(q), 0
         for b, (n, a) in enumerate(zip(lens, new)):
             k = self.ref.values(0, self.table[b], 0, n)
             v = self.ref.values(1, self.table[b], 0, n)
             top = self.ref.tops(1, self.table[b], 0, n)
-            y, mass, big, small = K.attention(q[at:at + a], k, v, n - a, scale, window, sinks, top)
+            y, mass, big, small = K.attention(q[at:at + a], k, v, n - a, scale, window, sinks, top,
+                                              None if keep is None else keep[b])
             out[at:at + a] = y
             # Weights rounded to fp16 (half a step: 2^-11) move y by 2^-11 sum w |v|. Below fp16's normal range the
             # error is 2^-25 against a largest weight of at least 1, weights there being w times the value scale:

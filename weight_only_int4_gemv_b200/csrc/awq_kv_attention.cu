@@ -492,7 +492,11 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     // only some of them the others' weights are 0 (one path for all keeps the code in the instruction cache).
     auto take = [&](auto count, int first) {
       constexpr int N = decltype(count)::value;
-      if (me.tile[first] < 0) return;
+      // (not the first alone: its page may be missing and the next one's there)
+      bool any = false;
+#pragma unroll
+      for (int u = 0; u < N; ++u) any |= me.tile[first + u * W] >= 0;
+      if (!any) return;
       const uint8_t* kt[N];
       const uint8_t* vt[N];
       int tile[N];
