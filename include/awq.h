@@ -485,9 +485,10 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
  *
  * Values out of range in these arrays (a page id outside 0 .. n_pages - 1, a
  * length above max_pages * page_size, offsets that descend or pass n_tokens)
- * never lead outside the buffers: the tokens they concern are skipped, bit 4
- * of awq_device_error is set, and the outputs of the sequences concerned are
- * unspecified.
+ * never lead outside the buffers: the tokens they concern are skipped, and bit
+ * 4 of awq_device_error is set. Keys whose page id is out of range are to
+ * attention as if masked; what else concerns the sequence (offsets, a length)
+ * leaves its outputs unspecified.
  *
  * 16-bit rows (q, k, v, outputs) have their heads x head_dim values dense,
  * rows `stride` values apart (a multiple of 8), so the columns of a fused

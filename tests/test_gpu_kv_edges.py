@@ -1,5 +1,6 @@
 """awq_kv_attention where a cache or a table holds what is allowed but unusual,
-against the float64 oracle, in tiles of 8 and of 16 rows."""
+against the float64 oracle. Each test runs the few-row kernel (tiles of 8 and
+of 16 rows) and the many-row one."""
 
 import numpy as np
 import pytest
@@ -11,7 +12,7 @@ from test_gpu_kv_attention import queries
 
 pytestmark = pytest.mark.gpu
 
-KINDS = [1, 10]                     # rows of a sequence and head, at one query head to a key head
+KINDS = [1, 10, 70]                 # rows of a sequence and head, at one query head to a key head
 
 
 def is_many(cache, batch, tokens, heads):

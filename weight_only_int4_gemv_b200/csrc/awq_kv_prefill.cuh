@@ -58,7 +58,8 @@ enum : int {                                   // PreMeta::flags
   kBegin0 = 16, kBegin1 = 32,                  // the row tile's first tile of the segment
   kEnd0 = 64, kEnd1 = 128,                     // its last
   kHas0 = 256, kHas1 = 512,                    // the row tile has a tile in the segment
-  kStop = 1024                                 // no more tiles
+  kStop = 1024,                                // no more tiles
+  kHoles = 2048                                // a block's page id is out of range
 };
 
 // 1 / l; 0 for a row that sees nothing, NaN for one that sees a block without a finite scale.
@@ -71,6 +72,7 @@ struct alignas(16) PreMeta {     // (its arrays are read two floats at a time)
   int t0, row0, rows, past, head, dest;
   float ks[8], vs[8];            // the blocks' scales
   float a[8], lv[8], iv[8];      // scale log2(e) s_k, log2(s_v), 1 / s_v
+  uint32_t missing;              // with kHoles: bit i: block i has no page
 };
 
 template <int D>
@@ -384,7 +386,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       }
       if (flags & (x ? kAct1 : kAct0)) {
         const int pos = me.pos;
-        const bool all = pos + kTile - 1 <= p_low &&
+        const bool all = !(flags & kHoles) && pos + kTile - 1 <= p_low &&
                          (p.window == 0 || pos > p_high - p.window || pos + kTile <= p.sinks);
         const int k0 = half * (kTile / 2);             // the first key's column
         const int hi = p_row - pos - k0, lo = p.window ? hi - p.window + 1 : 0,
@@ -404,7 +406,11 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           // masked columns of S become the infinity that a's sign takes to -inf
 #pragma unroll 1
           for (int c = 0; c < kTile / 64; ++c) {
-            const uint32_t vis = low_bits(hi - 32 * c + 1) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+            uint32_t vis = low_bits(hi - 32 * c + 1) & (~low_bits(lo - 32 * c) | low_bits(sk - 32 * c));
+            if (flags & kHoles) {      // the keys of a missing block are whatever shared memory held
+              const uint32_t gone = me.missing >> (half * 4 + 2 * c);
+              vis &= ~((gone & 1u) * 0xffffu | ((gone >> 1) & 1u) * 0xffff0000u);
+            }
             if (__all_sync(0xffffffffu, vis == 0xffffffffu)) continue;
             uint32_t r[32];
             tc_ld32(ts + c * 32, r);
@@ -745,6 +751,8 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
               if (keys && lane < 16 && blk < s.len) page = checked_page(a, id, err);
               id = id_next;
               const unsigned here = __ballot_sync(0xffffffffu, page >= 0);
+              const unsigned missing = __ballot_sync(0xffffffffu, keys && lane < 8 && blk < s.len && page < 0);
+              if (missing) flags |= kHoles;
               if (!wait(&sh.meta_empty[mi], ((it / kMetaSlots) & 1) ^ 1)) {
                 ok = false;
                 break;
@@ -772,6 +780,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
                 me.past = s.past;
                 me.head = head;
                 me.dest = dest;
+                me.missing = missing;
               }
               __syncwarp();
               if (lane == 0) mbar_arrive(&sh.meta_full[mi]);
