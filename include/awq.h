@@ -466,9 +466,11 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
  *
  * pages page_stride bytes and scale_stride floats apart (the rest is dense),
  * so a layer's pages may be a slice of a larger array. A held value is
- *   AWQ_KV_INT8: s * (code - 128), codes 1 .. 255
+ *   AWQ_KV_INT8: s * (code - 128), codes 1 .. 255 from awq_kv_append
  *   AWQ_KV_E4M3: s * e4m3(code); the codes 0x7f and 0xff (NaN) are not written
  *                for finite values, and attention over them is unspecified
+ * A scale s is finite and 0 or positive. awq_kv_append writes none below 2^-60;
+ * a cache filled otherwise may hold 0, with any code, for a block of zeros.
  * head_dim is 64 or 128; page_size a multiple of 16, up to 65536.
  *
  * A batch says which tokens a call is about. Sequence b holds seq_lens[b]

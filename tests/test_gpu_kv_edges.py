@@ -30,6 +30,13 @@ def attend(s, q, lens, new, table=None, window=0, sinks=0):
     return awq.awq_kv_attention(q, s.cache, batch, window=window, sinks=sinks)
 
 
+def put(s):
+    """The oracle's codes and scales into the device's cache."""
+    for t, a in ((s.cache.k_pages, s.ref.codes[0]), (s.cache.v_pages, s.ref.codes[1]),
+                 (s.cache.k_scales, s.ref.scales[0]), (s.cache.v_scales, s.ref.scales[1])):
+        t.copy_(torch.from_numpy(a))
+
+
 @pytest.mark.parametrize("rows", KINDS)
 @pytest.mark.parametrize("dtype,fmt,dim", [("fp16", "int8", 128), ("bf16", "e4m3", 64)])
 @pytest.mark.parametrize("window,sinks", [(0, 0), (100, 20)])
@@ -53,3 +60,24 @@ def test_pages_out_of_range_are_as_if_masked(rows, dtype, fmt, dim, window, sink
     assert awq.awq_device_error() == 16
     want, tol = s.expect(to64(q), lens, new, window=window, sinks=sinks, keep=keep)
     check(got, want, tol)
+
+
+@pytest.mark.parametrize("rows", KINDS)
+@pytest.mark.parametrize("dtype,fmt,dim", [("fp16", "int8", 128), ("bf16", "e4m3", 64)])
+def test_scales_of_zero(rows, dtype, fmt, dim):
+    """A block of scale 0 holds zeros whatever its codes: its keys have logits of 0, its values count as 0 with their
+    keys' weights."""
+    lens, new = [300, 84, 20], [rows, min(rows, 33), 1]
+    s = Setup(lens, 2, dim, 16, fmt, seed=42)
+    for w, blocks in ((0, [(0, 2), (0, 7), (1, 0)]), (1, [(0, 3), (0, 7), (0, 8), (1, 1), (2, 0), (2, 1)])):
+        for b, i in blocks:
+            s.ref.scales[w][int(s.table[b, i]), i % 2 if b < 2 else slice(None)] = 0.0
+    # codes that an own quantizer may leave in such a block
+    s.ref.codes[1][int(s.table[0, 3]), 1] = 0
+    s.ref.codes[1][int(s.table[0, 8]), 0] = 255 if fmt == "int8" else 0x7e
+    put(s)
+    q = queries(s.rng, sum(new), 2, dim, dtype)
+    want, tol = s.expect(to64(q), lens, new)
+    assert (want[-1] == 0).all()
+    check(attend(s, q, lens, new), want, tol)
+    assert awq.awq_device_error() == 0

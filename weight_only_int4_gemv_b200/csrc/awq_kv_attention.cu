@@ -501,6 +501,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       const uint8_t* vt[N];
       int tile[N];
       float ks[N], lv[N], iv[N];
+      uint32_t held[N];
 #pragma unroll
       for (int u = 0; u < N; ++u) {
         const int i = first + u * W;
@@ -508,7 +509,10 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         vt[u] = &sh.ring[s][(WT + i) * Sh::kTile];
         tile[u] = me.tile[i];
         ks[u] = tile[u] < 0 ? 0.0f : me.ks[i];
-        const float vs = tile[u] < 0 ? 1.0f : me.vs[i];
+        float vs = tile[u] < 0 ? 1.0f : me.vs[i];
+        // (values of scale 0 are 0 whatever their codes: no weight in O; in l they have their keys', by the smallest scale)
+        held[u] = vs == 0.0f ? 0u : ~0u;
+        vs = vs == 0.0f ? kScaleFloor : vs;
         lv[u] = __log2f(vs);
         // (O holds codes / kShift; a scale that is no positive number must not reach the rows that do not see its block)
         iv[u] = vs > 0.0f ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;
@@ -593,8 +597,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
           for (int e = 0; e < 4; ++e) w[e] = exp2_fast(sc[u][nt][e] - base[e & 1]);
           l[nt][0] = fmaf(w[0] + w[2], iv[u], l[nt][0]);
           l[nt][1] = fmaf(w[1] + w[3], iv[u], l[nt][1]);
-          b0[u][nt] = transpose8x8(Half16<__half>::pack(w[0], w[1]));
-          b1[u][nt] = transpose8x8(Half16<__half>::pack(w[2], w[3]));
+          b0[u][nt] = transpose8x8(Half16<__half>::pack(w[0], w[1])) & held[u];
+          b1[u][nt] = transpose8x8(Half16<__half>::pack(w[2], w[3])) & held[u];
         }
       }
       // O += V^T p: lane (g, t) holds channels [D/8 g, D/8 (g + 1)) of keys 2t, 2t+1, 2t+8, 2t+9

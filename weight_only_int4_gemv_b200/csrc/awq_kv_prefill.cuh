@@ -580,16 +580,19 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const PreMeta& me = sh.meta[mi];
       const int flags = me.flags;
       if (flags & kStop) break;
+      const unsigned zeros = __ballot_sync(0xffffffffu, lane < 8 && me.vs[lane & 7] == 0.0f);
       if (tid < 8) {                             // (published with the keys)
         PreMeta& out = sh.meta[mi];
         // A scale that is not finite must not reach the rows that do not see its block (there t is -inf by S, whatever
         // finite numbers stand here) and has to show in the others: their m becomes kSpoilt, which ends as NaN.
         const float ks = me.ks[tid], vs = me.vs[tid];
-        const bool fine = ks - ks == 0.0f && vs - vs == 0.0f && vs > 0.0f;
+        const bool fine = ks - ks == 0.0f && vs - vs == 0.0f && vs >= 0.0f;
         const float a = fine ? fmaxf(fabsf(p.scale_log2) * kShift<FMT> * ks, kLeastA) : kLeastA;
         out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
-        out.lv[tid] = fine ? __log2f(vs) : kSpoilt;
-        out.iv[tid] = fine ? __fdividef(1.0f / kShift<FMT>, vs) : 1.0f;   // (O holds codes / kShift)
+        // (a scale of 0 counts as the smallest one here, which gives its keys their mass; its codes are made 0 below)
+        const float v = vs == 0.0f ? kScaleFloor : vs;
+        out.lv[tid] = fine ? __log2f(v) : kSpoilt;
+        out.iv[tid] = fine ? __fdividef(1.0f / kShift<FMT>, v) : 1.0f;   // (O holds codes / kShift)
       }
       __syncwarp();
       if (lane == 0) mbar_arrive(&sh.meta_empty[mi]);
@@ -611,6 +614,13 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           widen16<FMT>(w, a, b);
           *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c0) = a;
           *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c1) = b;
+        }
+        if (kv && zeros) {                        // values of scale 0 are 0, whatever their codes
+#pragma unroll 1
+          for (int i = 0; i < kTile / kRowStep; ++i)
+            if ((zeros >> ((r0 + i * kRowStep) / kBlock)) & 1u)
+              *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c0) =
+                  *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c1) = make_uint4(0, 0, 0, 0);
         }
         fence_proxy_async_smem();
         __syncwarp();
