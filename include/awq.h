@@ -471,6 +471,8 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
  *                for finite values, and attention over them is unspecified
  * A scale s is finite and 0 or positive. awq_kv_append writes none below 2^-60;
  * a cache filled otherwise may hold 0, with any code, for a block of zeros.
+ * NaN, an infinity or a negative number in place of a scale makes NaN of the
+ * attention of every row and query head that sees the block, and of no other.
  * head_dim is 64 or 128; page_size a multiple of 16, up to 65536.
  *
  * A batch says which tokens a call is about. Sequence b holds seq_lens[b]
@@ -555,8 +557,9 @@ typedef struct awq_kv_rope {
  * fp32, then to the code) and clamped to the codes' range. Appending the same
  * rows at the same positions again leaves the same cache. A NaN or an infinity
  * among x makes s, and what is read from the block's head, NaN or infinite
- * until the block is written again from its first token; other blocks and
- * heads, and attention rows that do not see the block, are as without it.
+ * until the block is written again from its first token (attention rows that
+ * see the block become NaN); other blocks and heads, and attention rows that
+ * do not see the block, are as without it.
  * k, v [n_tokens][n_kv_heads][head_dim]. q [n_tokens][n_q_heads][head_dim]
  * and q_out (the same shape; may be q itself) are both given or both NULL;
  * q_out = q turned, rounded once. rope NULL: nothing is turned. Only the

@@ -81,3 +81,48 @@ def test_scales_of_zero(rows, dtype, fmt, dim):
     assert (want[-1] == 0).all()
     check(attend(s, q, lens, new), want, tol)
     assert awq.awq_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", KINDS)
+@pytest.mark.parametrize("which", ["k_scales", "v_scales"])
+@pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf"), -1.0])
+@pytest.mark.parametrize("dtype,fmt", [("fp16", "int8"), ("bf16", "e4m3")])
+def test_a_spoilt_block_shows_in_every_row_that_sees_it(rows, which, value, dtype, fmt):
+    """A scale that is no non-negative number makes NaN of all rows of its head that see the block, and of no other."""
+    lens, new = [100 + rows], [rows]
+    for block in (4, 6):                  # 64 .. 79, which the window leaves, and 96 .. 111, which the first rows reach
+        s = Setup(lens, 2, 128, 16, fmt, seed=43)
+        getattr(s.cache, which)[int(s.table[0, block]), 0] = value
+        q = queries(s.rng, rows, 2, 128, dtype)
+        want, tol = s.expect(to64(q), lens, new, window=50)
+        got = attend(s, q, lens, new, window=50)
+        p = 100 + np.arange(rows)
+        sees = (p >= 16 * block) & (p - 50 < 16 * block + 15)
+        check(got[:, 1:], want[:, 1:], tol[:, 1:], "the other head")
+        clean, bad = np.flatnonzero(~sees), np.flatnonzero(sees)
+        assert len(bad)
+        check(got[torch.from_numpy(clean).cuda(), :1], want[clean, :1], tol[clean, :1], "rows that do not see it")
+        y = got[torch.from_numpy(bad).cuda(), 0]
+        assert torch.isnan(y).all(), f"block {block}: {(~torch.isnan(y)).sum()} values are no NaN"
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("sign", [1, -1])
+def test_a_first_token_with_an_infinity_shows(many, fmt, sign):
+    """A token that opens a block, with an infinity in its key: no other token's zero code lies in the block."""
+    n = 33
+    new = 97 if many else 1                # a prompt up to that token, or the token alone
+    lens = [n + 64] if many else [n]
+    s = Setup(lens, 1, 64, 16, fmt, seed=44)
+    rows = torch.from_numpy(s.rng.standard_normal((2, lens[0], 1, 64))).cuda().half()
+    batch = s.batch(lens, lens)
+    awq.awq_kv_append(rows[0], rows[1], s.cache, batch)
+    rows[0, -1, 0, 5] = float("inf")
+    awq.awq_kv_append(rows[0, -1:], rows[1, -1:], s.cache, s.batch(lens, [1]))
+    q = queries(s.rng, new, 1, 64, "fp16")
+    q[:, 0, 5] = 2.0 * sign
+    got = attend(s, q, lens, [new])
+    assert torch.isnan(got[-1]).all()
+    if many:
+        assert torch.isfinite(got[:-1]).all()

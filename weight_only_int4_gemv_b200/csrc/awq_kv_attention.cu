@@ -508,14 +508,17 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         kt[u] = &sh.ring[s][i * Sh::kTile];
         vt[u] = &sh.ring[s][(WT + i) * Sh::kTile];
         tile[u] = me.tile[i];
-        ks[u] = tile[u] < 0 ? 0.0f : me.ks[i];
-        float vs = tile[u] < 0 ? 1.0f : me.vs[i];
-        // (values of scale 0 are 0 whatever their codes: no weight in O; in l they have their keys', by the smallest scale)
+        const bool there = tile[u] >= 0;
+        ks[u] = there ? me.ks[i] : 0.0f;
+        float vs = there ? me.vs[i] : 1.0f;
+        // values of scale 0 are 0 whatever their codes: no weight in O; in l they have their keys', by the smallest scale
         held[u] = vs == 0.0f ? 0u : ~0u;
         vs = vs == 0.0f ? kScaleFloor : vs;
-        lv[u] = __log2f(vs);
-        // (O holds codes / kShift; a scale that is no positive number must not reach the rows that do not see its block)
-        iv[u] = vs > 0.0f ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;
+        // a scale that is no finite number of at least 0 makes NaN of the logits, which the rows that do not see the
+        // block mask (an infinite one times a negative S would be a weight of 0 instead)
+        const bool fine = ks[u] >= 0.0f && vs >= 0.0f && ks[u] + vs < INFINITY;
+        lv[u] = fine ? __log2f(vs) : __int_as_float(0x7fffffff);
+        iv[u] = fine ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;   // (O holds codes / kShift)
       }
       // S = K q^T
       float sc[N][NT][4];

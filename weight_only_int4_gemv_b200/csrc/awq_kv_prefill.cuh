@@ -62,7 +62,7 @@ enum : int {                                   // PreMeta::flags
   kHoles = 2048                                // a block's page id is out of range
 };
 
-// 1 / l; 0 for a row that sees nothing, NaN for one that sees a block without a finite scale.
+// 1 / l; 0 for a row that sees nothing, NaN for one that sees a spoilt block.
 __device__ __forceinline__ float inverse(float m, float l) {
   return m == -INFINITY ? 0.0f : m >= kSpoilt ? __uint_as_float(0x7fffffffu) : __fdiv_rn(1.0f, l);
 }
@@ -583,10 +583,10 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const unsigned zeros = __ballot_sync(0xffffffffu, lane < 8 && me.vs[lane & 7] == 0.0f);
       if (tid < 8) {                             // (published with the keys)
         PreMeta& out = sh.meta[mi];
-        // A scale that is not finite must not reach the rows that do not see its block (there t is -inf by S, whatever
+        // A scale that is no finite number of at least 0 must not reach the rows that do not see its block (there t is -inf by S, whatever
         // finite numbers stand here) and has to show in the others: their m becomes kSpoilt, which ends as NaN.
         const float ks = me.ks[tid], vs = me.vs[tid];
-        const bool fine = ks - ks == 0.0f && vs - vs == 0.0f && vs >= 0.0f;
+        const bool fine = ks >= 0.0f && vs >= 0.0f && ks + vs < INFINITY;
         const float a = fine ? fmaxf(fabsf(p.scale_log2) * kShift<FMT> * ks, kLeastA) : kLeastA;
         out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
         // (a scale of 0 counts as the smallest one here, which gives its keys their mass; its codes are made 0 below)
