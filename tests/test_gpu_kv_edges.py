@@ -22,12 +22,12 @@ def is_many(cache, batch, tokens, heads):
     return n % (32 + 2 * 256 * (cache.head_dim + 2) * 4) == 0
 
 
-def attend(s, q, lens, new, table=None, window=0, sinks=0):
+def attend(s, q, lens, new, table=None, window=0, sinks=0, scale=None):
     """The call, with a table wide enough that more than 64 rows take the many-row kernel."""
     many = max(new) > 64
     batch = s.batch(lens, new, max(new), table=table, wide=many)
     assert is_many(s.cache, batch, q.shape[0], q.shape[1]) == many
-    return awq.awq_kv_attention(q, s.cache, batch, window=window, sinks=sinks)
+    return awq.awq_kv_attention(q, s.cache, batch, scale=scale, window=window, sinks=sinks)
 
 
 def put(s):
@@ -126,3 +126,16 @@ def test_a_first_token_with_an_infinity_shows(many, fmt, sign):
     assert torch.isnan(got[-1]).all()
     if many:
         assert torch.isfinite(got[:-1]).all()
+
+
+@pytest.mark.parametrize("fmt,scale", [("e4m3", None), ("int8", 8.0), ("e4m3", -8.0)])
+def test_loudest_bf16_queries_over_keys_of_zero(fmt, scale):
+    """bf16 rows near the type's largest number have logits of 0 on keys of 0."""
+    for rows in KINDS:
+        s = Setup([150], 1, 64, 16, fmt, seed=45)
+        s.ref.codes[0][:] = 128 if fmt == "int8" else 0
+        s.ref.scales[0][:] = 2.0 ** -60
+        put(s)
+        q = (queries(s.rng, rows, 1, 64, "bf16").sign() * 2.0 ** 126).to(torch.bfloat16)
+        want, tol = s.expect(np.zeros((rows, 1, 64)), [150], [rows])
+        check(attend(s, q, [150], [rows], scale=scale), want, tol, str(rows))

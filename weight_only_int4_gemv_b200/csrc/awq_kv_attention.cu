@@ -448,8 +448,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 
   // -------------------------------------------------------------- consumers
   const int g = lane >> 2, t = lane & 3;
+  constexpr bool kScaled = std::is_same<T, __nv_bfloat16>::value;   // (fp16 rows enter as they are)
   uint32_t qf[NT][D / 8];
-  float factor[NT][2];               // of columns 2t, 2t + 1: logit scale in log2 units
+  float factor[NT][2];               // of columns 2t, 2t + 1: what q was divided by
   int at[NT][2];                     // positions of those rows
   float m[NT][2], l[NT][2];
   float acc[NT][D / 16][4];
@@ -475,7 +476,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         load_q<T, D>(sh.q[s] + (nt * 8 + g) * (D * 2), t, qf[nt], mine);
 #pragma unroll
         for (int e = 0; e < 2; ++e) {
-          factor[nt][e] = p.scale_log2 * kShift<FMT> * __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
+          if (kScaled) factor[nt][e] = __shfl_sync(0xffffffffu, mine, (2 * t + e) * 4);
           at[nt][e] = past + by_group(rem0 + nt * 8 + 2 * t + e);
           m[nt][e] = -INFINITY;
           l[nt][e] = 0.0f;
@@ -510,6 +511,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         tile[u] = me.tile[i];
         const bool there = tile[u] >= 0;
         ks[u] = there ? me.ks[i] : 0.0f;
+        const float to_log2 = p.scale_log2 * kShift<FMT>;   // (not into factor, which may be 2^126: keys of 0 have logits of 0)
         float vs = there ? me.vs[i] : 1.0f;
         // values of scale 0 are 0 whatever their codes: no weight in O; in l they have their keys', by the smallest scale
         held[u] = vs == 0.0f ? 0u : ~0u;
@@ -517,6 +519,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         // a scale that is no finite number of at least 0 makes NaN of the logits, which the rows that do not see the
         // block mask (an infinite one times a negative S would be a weight of 0 instead)
         const bool fine = ks[u] >= 0.0f && vs >= 0.0f && ks[u] + vs < INFINITY;
+        ks[u] *= to_log2;
         lv[u] = fine ? __log2f(vs) : __int_as_float(0x7fffffff);
         iv[u] = fine ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;   // (O holds codes / kShift)
       }
@@ -552,7 +555,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
 #pragma unroll
         for (int nt = 0; nt < NT; ++nt)
 #pragma unroll
-          for (int e = 0; e < 4; ++e) sc[u][nt][e] = fmaf(sc[u][nt][e], factor[nt][e & 1] * ks[u], lv[u]);
+          for (int e = 0; e < 4; ++e)
+            sc[u][nt][e] = fmaf(sc[u][nt][e], kScaled ? factor[nt][e & 1] * ks[u] : ks[u], lv[u]);
         if (!all) {
 #pragma unroll
           for (int nt = 0; nt < NT; ++nt)
