@@ -591,8 +591,9 @@ AWQ_API awq_status_t awq_kv_dequant(const awq_kv_cache_t* cache, const awq_kv_ba
  * q enters as it is (bf16 q through fp16 over a power of two per row, exact
  * for magnitudes down to 2^-17 of the row's largest); logits, softmax
  * statistics and sums are fp32; the weights, times the block's value scale,
- * are rounded to fp16 against a running maximum before they meet the value
- * codes.
+ * are rounded to fp16 before they meet the value codes (their sum takes them
+ * unrounded): each is off by at most the larger of 2^-11 of itself and 2^-32 of
+ * the row's largest.
  * q, out [n_tokens][n_q_heads][head_dim]; n_q_heads a multiple of
  * n_kv_heads; window, sinks >= 0 (sinks is ignored without a window);
  * scale finite. out must not overlap q.

@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import weight_only_int4_gemv_b200 as awq
-from kv_util import Setup, check, to64
+from kv_util import DT, Setup, check, to64
 from test_gpu_kv_attention import queries
 
 pytestmark = pytest.mark.gpu
@@ -139,3 +139,40 @@ def test_loudest_bf16_queries_over_keys_of_zero(fmt, scale):
         q = (queries(s.rng, rows, 1, 64, "bf16").sign() * 2.0 ** 126).to(torch.bfloat16)
         want, tol = s.expect(np.zeros((rows, 1, 64)), [150], [rows])
         check(attend(s, q, [150], [rows], scale=scale), want, tol, str(rows))
+
+
+@pytest.mark.parametrize("many", [False, True])
+@pytest.mark.parametrize("dtype,fmt", [("fp16", "int8"), ("bf16", "e4m3")])
+def test_a_long_tail_keeps_its_mass(many, dtype, fmt):
+    """A few keys with a weight of 1, 2^14 others with 2^-25.2 each, whose values alone are not 0: the output is their
+    share of the sum, about 2^-14. Weights are fp16 against a running maximum lifted to 2^7, where half a step of the
+    subnormal numbers is 2^-32 of the largest: 2^14 of them move y by 2^-18 at most; logits, statistics and the
+    weights' own rounding as in kv_util. As many sequences (of the same pages) as there are CTAs or so, so that a
+    sequence's keys meet one running maximum and are not cut into runs with maxima of their own."""
+    n, new, dim, seqs = (1 << 14) + 200, 70 if many else 1, 64, 148 if many else 592
+    s = Setup([n], 1, dim, 64, fmt, filled=False)
+    one, top, zero = (255, 127.0, 128) if fmt == "int8" else (0x7e, 448.0, 0)     # the largest code, its number, 0's
+    for t, c in ((s.cache.k_pages, zero), (s.cache.v_pages, one)):
+        t.fill_(c)
+    s.cache.k_scales.fill_(1.0 / top)
+    s.cache.v_scales.fill_(1.0 / top)
+    for token in (range(0, 64, 16) if many else range(0, 128, 16)):
+        page, at = int(s.table[0, token // 64]), token % 64
+        s.cache.k_pages[page, 0, at, 0] = one                # the loud keys: (1, 0, 0, ..), a block each, so that every
+        s.cache.v_pages[page, 0, at] = zero                  # warp of the few-row kernel meets one
+    loud = 4 if many else 8
+    q = torch.zeros(seqs * new, 1, dim, device="cuda", dtype=DT[dtype])
+    q[:, 0, 0] = 16.0
+    x = 25.2 * np.log(2.0)
+    scale = float(np.float32(x / 16.0))
+    batch = s.batch([n] * seqs, [new] * seqs, new, table=np.repeat(s.table, seqs, 0), wide=many)
+    assert is_many(s.cache, batch, q.shape[0], 1) == many
+    got = awq.awq_kv_attention(q, s.cache, batch, scale=scale)
+    assert awq.awq_device_error() == 0
+    seen = n - new + 1 + np.arange(new)                   # keys of each row
+    tail = (seen - loud) * np.exp(-16.0 * scale) / loud
+    want = tail / (1 + tail)
+    d = 2.0 ** -16 * x + 2.0 ** -17
+    tol = (2.0 ** -11 + 2 * d) * want + 2.0 ** -32 * seen
+    shape = (seqs, new, 1, dim)
+    check(got, *(np.broadcast_to(a[None, :, None, None], shape).reshape(got.shape) for a in (want, tol)))

@@ -5,12 +5,14 @@
 // group) pairs, R of them to a tile. For a tile of 16 keys (one scale block)
 //   S = K_codes q^T            exact products, fp32 sums (tensor cores)
 //   t_j = scale log2(e) s_k S_j + log2(s_v)
-//   p_j = 2^(t_j - m),  O += V_codes^T p,  l += p_j / s_v
+//   p_j = 2^(t_j - m + 7),  O += V_codes^T p,  l += p_j / s_v
 // with a running maximum m of t, and y = O / l at the end: the value scale
 // rides on the weight (sum 2^(t'_j) s_v c_j / sum 2^(t'_j), t' = t - log2
-// s_v), so the codes enter the second product as they are, and p <= 2^8 fits
+// s_v), so the codes enter the second product as they are, and p <= 2^15 fits
 // fp16 whatever the scales. m is only raised when a logit passes it by more
-// than 8 (then O and l are rescaled); below that p stays within fp16.
+// than 8 (then O and l are rescaled); below that p stays within fp16. The lift
+// by 2^7 is for long contexts: fp16 holds p down to 2^-25, so what is rounded
+// off a weight is at most 2^-32 of the largest's, and n keys lose n 2^-32.
 //
 // What bounds it: for the few rows of decoding, reading the cache. Both
 // products have the codes as the 16-row operand of mma.sync.m16n8k16 (16 keys
@@ -69,6 +71,7 @@ constexpr int kItemCost = 12;
 constexpr int kItems = 8;                  // more than the stages in the ring and the one ahead of it
 constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
+constexpr float kLift = 7.0f;              // log2 of the weight at m: with kSlack, the largest that fp16 has room for
 
 struct AttentionParams {
   Batch batch;
@@ -596,7 +599,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       uint32_t b0[N][NT], b1[N][NT];
 #pragma unroll
       for (int nt = 0; nt < NT; ++nt) {
-        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0], m[nt][1] == -INFINITY ? 0.0f : m[nt][1]};
+        const float base[2] = {m[nt][0] == -INFINITY ? 0.0f : m[nt][0] - kLift,
+                               m[nt][1] == -INFINITY ? 0.0f : m[nt][1] - kLift};
 #pragma unroll
         for (int u = 0; u < N; ++u) {
           float w[4];

@@ -2,7 +2,7 @@
 // included by awq_kv_attention.cu inside namespace awq::kv.
 //
 // Mathematics: as for few rows (t = scale log2(e) s_k S + log2(s_v), p = 2^(t
-// - m), y = sum p c_v / sum (p / s_v)), over tiles of 128 rows by 128 keys.
+// - m + 7), y = sum p c_v / sum (p / s_v)), over tiles of 128 rows by 128 keys.
 //
 // What bounds it: two products of 128 x 128 x head_dim and 128 x 128
 // exponentials per tile, about equal at the tensor and the special-function
@@ -468,7 +468,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           m = raised;
         }
         // The weights, over the S columns.
-        const float base = m == -INFINITY ? 0.0f : m;
+        const float base = m == -INFINITY ? 0.0f : m - kLift;
 #pragma unroll 1
         for (int c = 0; c < kTile / 64; ++c) {
           uint32_t r[32], pk[16];
