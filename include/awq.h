@@ -320,10 +320,12 @@ AWQ_API awq_status_t awq_gemv_chain(const awq_gemv_layer_t* layers, int n_layers
 
 /*
  * awq_debug_set_wait_limit_ns -- test hook: the time limit after which a
- * pipeline wait inside awq_gemv_chain gives up (0 restores the default of
- * 2 s; at most 2 s). Copies already in flight are always waited for with
- * the full limit. Synchronizes `stream`. The pages have no counterpart; it
- * exists so that tests can make a wait run out without a fault.
+ * pipeline wait inside awq_gemv_chain (on the current device) or
+ * awq_kv_attention (on any device, in calls made after it) gives up (0
+ * restores the default of 2 s; at most 2 s). Copies already in flight are
+ * always waited for with the full limit. Synchronizes `stream`. The pages
+ * have no counterpart; it exists so that tests can make a wait run out
+ * without a fault.
  */
 AWQ_API awq_status_t awq_debug_set_wait_limit_ns(uint64_t ns, void* stream);
 

@@ -176,3 +176,31 @@ def test_a_long_tail_keeps_its_mass(many, dtype, fmt):
     tol = (2.0 ** -11 + 2 * d) * want + 2.0 ** -32 * seen
     shape = (seqs, new, 1, dim)
     check(got, *(np.broadcast_to(a[None, :, None, None], shape).reshape(got.shape) for a in (want, tol)))
+
+
+@pytest.mark.parametrize("rows", KINDS)
+def test_waits_give_up_and_recover(rows):
+    """Pipeline waits made to run out without a fault: with a limit of 1 ns the first wait for a slot, or a place for
+    q rows, that is not free gives up, other copies in flight; with longer ones a later wait may. The call records bit
+    3, lets its copies and products land and returns; with the limit restored the next call gives the bits of the one
+    before. Sequences share their pages and are many, so that CTAs have more tiles than slots and several items."""
+    seqs = 48
+    lens, new = [3000] * seqs, [rows] * seqs
+    s = Setup([3000], 2, 128, 16, "int8", seed=47)
+    s.table = np.repeat(s.table, seqs, 0)
+    q = queries(s.rng, sum(new), 2, 128, "bf16")
+    first = attend(s, q, lens, new)
+    want, tol = s.expect(to64(q[:rows]), lens[:1], new[:1])
+    check(first[:rows], want, tol)
+    assert awq.awq_device_error() == 0
+    for limit in (1, 1, 500, 1000, 2000, 4000):
+        try:
+            awq.awq_debug_set_wait_limit_ns(limit)
+            attend(s, q, lens, new)
+            torch.cuda.synchronize()
+            error = awq.awq_device_error()
+        finally:
+            awq.awq_debug_set_wait_limit_ns(0)
+        assert error == 8 or limit > 1 and error == 0, limit
+        assert torch.equal(attend(s, q, lens, new), first)
+        assert awq.awq_device_error() == 0

@@ -664,8 +664,9 @@ def awq_gemv_chain(M: int, layers, weights_static: bool = False):
 
 
 def awq_debug_set_wait_limit_ns(ns: int, device=None):
-    """Test hook: the time limit of awq_gemv_chain's pipeline waits (0: the
-    default 2 s). Synchronizes the device's current stream."""
+    """Test hook: the time limit of the pipeline waits of awq_gemv_chain (on
+    the device) and of awq_kv_attention's later calls (0: the default 2 s).
+    Synchronizes the device's current stream."""
     dev = device if device is not None else torch.cuda.current_device()
     with torch.cuda.device(dev):
         _check("awq_debug_set_wait_limit_ns", lib().awq_debug_set_wait_limit_ns(int(ns), _stream(dev)))

@@ -1259,9 +1259,16 @@ extern "C" awq_status_t awq_gemv_chain(const awq_gemv_layer_t* layers, int n_lay
   return launch_status();
 }
 
+namespace awq {
+namespace kv {
+void attention_set_wait_limit(uint64_t ns);   // awq_kv_attention.cu
+}  // namespace kv
+}  // namespace awq
+
 extern "C" awq_status_t awq_debug_set_wait_limit_ns(uint64_t ns, void* stream) {
   if (ns == 0) ns = kWaitLimitNs;
   if (ns > kWaitLimitNs) return AWQ_ERR_SHAPE;
+  kv::attention_set_wait_limit(ns);
   const unsigned long long v = ns;
   cudaStream_t s = static_cast<cudaStream_t>(stream);
   if (cudaMemcpyToSymbolAsync(g_awq_chain_wait_limit_ns, &v, sizeof(v), 0, cudaMemcpyHostToDevice, s) != cudaSuccess)

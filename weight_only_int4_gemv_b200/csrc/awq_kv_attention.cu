@@ -73,6 +73,12 @@ constexpr float kLog2e = 1.4426950408889634f;
 constexpr float kSlack = 8.0f;             // how far a logit may pass m (log2 units)
 constexpr float kLift = 7.0f;              // log2 of the weight at m: with kSlack, the largest that fp16 has room for
 
+// How long a pipeline wait lasts before it gives up (awq_debug_set_wait_limit_ns shortens it for tests).
+struct WaitLimit {
+  uint32_t polls;                          // polls between two looks at the clock; 1: a shortened limit
+  long long cycles;
+};
+
 struct AttentionParams {
   Batch batch;
   const uint16_t* q;
@@ -88,6 +94,7 @@ struct AttentionParams {
   int32_t whole;                           // few rows: a CTA takes whole items (no parts, no join)
   float* part;                             // [2 grid][R][D + 2] fp32
   struct Join* joins;                      // [grid]
+  WaitLimit wait;
 };
 
 // A split item, described by the CTA in whose run it starts.
@@ -144,29 +151,54 @@ struct Shared {
   int abort;
 };
 
-constexpr long long kWaitCycles = 4000000000ll;   // about 2 s
-
 // A bounded wait in few instructions: it is inlined in many places, and a
-// warp that polls shares its scheduler with one that works.
-__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, volatile int* abort, uint32_t* err) {
+// warp that polls shares its scheduler with one that works. LIMITED: one
+// wait of each kernel off its critical path (for a free slot, few rows; for
+// the place of the next segment's q rows, many), which a shortened limit makes
+// run out; its polls do not sleep then (a poll that sleeps may do so for longer
+// than its hint). The others see the abort flag. (With that form in every wait
+// the many-row kernel takes 13 % longer, in the few-row consumers' alone 3 %.)
+template <bool LIMITED = false>
+__device__ __forceinline__ bool wait_small(uint64_t* bar, uint32_t parity, const WaitLimit& limit, volatile int* abort,
+                                           uint32_t* err) {
   for (long long t0 = 0;;) {
     uint32_t ok;
-    asm volatile(
-        "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
-        "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
-        "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t@q bra POLL_%=;\n"
-        "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
-        : "=r"(ok)
-        : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
-        : "memory");
+    if constexpr (LIMITED) {
+      asm volatile(
+          "{\n\t.reg .pred p, q, w;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n\tsetp.ne.u32 w, %4, 1;\n"
+          "POLL_%=:\n\t@w mbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "@!w mbarrier.test_wait.parity.shared::cta.b64 p, [%1], %2;\n\t"
+          "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, %4;\n\t@q bra POLL_%=;\n"
+          "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u), "r"(limit.polls)
+          : "memory");
+    } else {
+      asm volatile(
+          "{\n\t.reg .pred p, q;\n\t.reg .u32 n;\n\tmov.u32 n, 0;\n"
+          "POLL_%=:\n\tmbarrier.try_wait.parity.shared::cta.b64 p, [%1], %2, %3;\n\t"
+          "@p bra DONE_%=;\n\tadd.u32 n, n, 1;\n\tsetp.lt.u32 q, n, 256;\n\t@q bra POLL_%=;\n"
+          "DONE_%=:\n\tselp.u32 %0, 1, 0, p;\n\t}"
+          : "=r"(ok)
+          : "r"(smem_u32(bar)), "r"(parity), "r"(1000000u)
+          : "memory");
+    }
     if (ok) return true;
     const long long t = clock64();
     if (t0 == 0) t0 = t;
-    if (t - t0 > kWaitCycles || *abort) {
+    if (t - t0 > (LIMITED ? limit.cycles : 2 * static_cast<long long>(kWaitLimitNs)) || *abort) {
       *abort = 1;
       atomicOr(err, kErrWait);
       return false;
     }
+  }
+}
+
+// Copies or products under way are waited for before a CTA ends, by the clock
+// of the SM (the global timer takes about a microsecond to read).
+__device__ __forceinline__ void drain(uint64_t* bar, uint32_t parity) {
+  for (const long long t0 = clock64();
+       !mbar_try_wait_sleep(bar, parity) && clock64() - t0 < 2 * static_cast<long long>(kWaitLimitNs);) {
   }
 }
 
@@ -283,7 +315,7 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
   pdl_wait();
   // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
+    return __all_sync(0xffffffffu, wait_small(bar, parity, p.wait, abort, err)) != 0;
   };
 
   // row / group for the rows of a tile, counted from a token's first (below 2^17: a float's product is exact enough)
@@ -311,7 +343,6 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
     join.last = -1;
     int s = 0;
     uint32_t ph = 0, used = 0;       // used: stages filled at least once
-    bool ok = true;
     if (b_first >= 0) {
       int b = b_first;
       Seq seq = load_seq(p.batch, b, err);
@@ -392,10 +423,8 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       while (go) {
         go = more;
         if (go) next(after);
-        if (!wait(&sh.empty[s], ph ^ 1)) {
-          ok = false;
-          break;
-        }
+        const bool free_slot = wait_small<true>(&sh.empty[s], ph ^ 1, p.wait, abort, err);
+        if (!__all_sync(0xffffffffu, free_slot)) break;
         int page = -1;
         if (cur.pos >= 0) page = checked_page(p.batch, cur.id, err);
         auto& m = sh.meta[s];
@@ -441,11 +470,9 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
       }
     }
     if (lane == 0 && !p.whole) p.joins[blockIdx.x] = join;
-    if (!ok) {
-      // every copy issued lands before the CTA's shared memory goes
-      for (int k = 0; k < kStages; ++k)
-        if (used & (1u << k)) wait_sleep_teardown(&sh.full[k], k < s ? ph : ph ^ 1);
-    }
+    // Every copy issued lands before the CTA's shared memory goes: the other warps may have given up on the last ones.
+    for (int k = 0; k < kStages; ++k)
+      if (used & (1u << k)) drain(&sh.full[k], k < s ? ph : ph ^ 1);
     return;
   }
 
@@ -851,6 +878,14 @@ awq_status_t resident(const Variant& v, int key, int* grid) {
   return AWQ_OK;
 }
 
+// What awq_debug_set_wait_limit_ns asks for, on every device.
+std::atomic<uint64_t> g_wait_limit_ns{kWaitLimitNs};
+
+WaitLimit wait_limit() {
+  const uint64_t ns = g_wait_limit_ns.load(std::memory_order_relaxed);
+  return {ns == kWaitLimitNs ? 256u : 1u, 2 * static_cast<long long>(ns)};   // about two cycles a nanosecond
+}
+
 size_t workspace_of(const Variant& v, int grid, int d) {
   return size_t(grid) * sizeof(Join) + size_t(grid) * 2 * v.R * (d + 2) * sizeof(float);
 }
@@ -913,6 +948,8 @@ awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, i
 }
 
 }  // namespace
+
+void attention_set_wait_limit(uint64_t ns) { g_wait_limit_ns.store(ns, std::memory_order_relaxed); }
 
 awq_status_t attention_take_error(uint32_t* word, cudaStream_t s) {
   const uint32_t zero = 0;
@@ -983,6 +1020,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   p.group = n_q_heads / cache->n_kv_heads;
   p.n_kv_heads = cache->n_kv_heads;
   p.whole = plan.whole;
+  p.wait = wait_limit();
   p.inv_group = 1.0f / float(p.group);
   p.joins = static_cast<Join*>(workspace);
   p.part = reinterpret_cast<float*>(static_cast<uint8_t*>(workspace) + size_t(plan.grid) * sizeof(Join));

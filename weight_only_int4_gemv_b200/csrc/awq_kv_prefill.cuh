@@ -355,7 +355,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
   const uint32_t tmem = sh.tmem;
   // one answer for the whole warp, so that its collective instructions stay together when a wait gives up
   auto wait = [&](uint64_t* bar, uint32_t parity) {
-    return __all_sync(0xffffffffu, wait_small(bar, parity, abort, err)) != 0;
+    return __all_sync(0xffffffffu, wait_small(bar, parity, p.wait, abort, err)) != 0;
   };
 
   if (warp < kSoftmaxWarps) {
@@ -828,13 +828,14 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     }
     // every copy issued has landed before the CTA's shared memory goes
     for (int i = max(0, n - kRawSlots); i < n; ++i)
-      wait_sleep_teardown(&sh.raw_full[i % kRawSlots], (i / kRawSlots) & 1);
+      drain(&sh.raw_full[i % kRawSlots], (i / kRawSlots) & 1);
+    asm volatile("cp.async.wait_all;" ::: "memory");
   } else if (warp == kSoftmaxWarps + kWidenWarps + 1) {
     // ----------------------------------------------------------- the products
     // QK of a tile is issued one tile ahead of its PV, interleaved by row tile:
     // S0(j+1) right behind O0(j), while softmax 1 works on tile j.
     if (elect_one()) {
-    auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_small(bar, parity, abort, err); };
+    auto wait1 = [&](uint64_t* bar, uint32_t parity) { return wait_small(bar, parity, p.wait, abort, err); };
     // bit x: parity of the row tile's next q rows, weights, free O; whether its O was used before (bits, because an
     // array indexed by x would live in local memory)
     uint32_t q_ph = 0, p_ph = 0, of_ph = 0, used_o = 0;
@@ -926,7 +927,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
     }
     // everything issued has finished before tensor memory is given back
     tc_commit(&sh.done);
-    wait_sleep_teardown(&sh.done, 0);
+    drain(&sh.done, 0);
     }
   } else {
     // ------------------------------------------------------------------ q rows
@@ -949,7 +950,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         for (int x = 0; x < 2 && ok; ++x) {
           if (!(flags & (x ? kHas1 : kHas0))) continue;
           if (used[x]++) {
-            ok = wait(&sh.q_free[x], q_ph[x]);
+            ok = __all_sync(0xffffffffu, wait_small<true>(&sh.q_free[x], q_ph[x], p.wait, abort, err));
             q_ph[x] ^= 1;
             if (!ok) break;
           }
