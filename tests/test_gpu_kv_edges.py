@@ -1,6 +1,6 @@
 """awq_kv_attention where a cache or a table holds what is allowed but unusual,
-against the float64 oracle. Each test runs the few-row kernel (tiles of 8 and
-of 16 rows) and the many-row one."""
+and awq_kv_dequant's rounding, against the float64 oracle. Each attention test
+runs the few-row kernel (tiles of 8 and of 16 rows) and the many-row one."""
 
 import numpy as np
 import pytest
@@ -204,3 +204,19 @@ def test_waits_give_up_and_recover(rows):
         assert error == 8 or limit > 1 and error == 0, limit
         assert torch.equal(attend(s, q, lens, new), first)
         assert awq.awq_device_error() == 0
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+@pytest.mark.parametrize("dtype", [torch.float16, torch.bfloat16])
+def test_dequant_rounds_once(fmt, dtype):
+    """Each value is one rounding of the exact product: float64 holds it (24 + 8 bits), and rounds it to 16 bits once."""
+    n = 4096
+    s = Setup([n], 2, 64, 64, fmt, seed=46)
+    k, v = awq.awq_kv_dequant(s.cache, s.batch([n], [n]), n, dtype)
+    for w, y in ((0, k), (1, v)):
+        exact = s.ref.values(w, s.table[0], 0, n)
+        mantissa = 11 if dtype is torch.float16 else 8
+        lowest = -14 if dtype is torch.float16 else -126
+        e = np.maximum(np.floor(np.log2(np.abs(np.where(exact == 0, 1.0, exact)))), lowest) - (mantissa - 1)
+        want = np.rint(exact / 2.0 ** e) * 2.0 ** e       # a power of two divides exactly; ties to even
+        assert np.array_equal(to64(y), want), f"{(to64(y) != want).sum()} values"

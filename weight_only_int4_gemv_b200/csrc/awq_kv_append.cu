@@ -142,6 +142,13 @@ __device__ __forceinline__ float quotient(float hi, float lo, float s, float inv
   return __uint_as_float(bits);
 }
 
+// a b cut off to fp32 with the last bit set where anything was cut (rounded to
+// odd), so that rounding it to 16 bits rounds the product itself.
+__device__ __forceinline__ float product_to_odd(float a, float b) {
+  const float p = __fmul_rz(a, b), r = fmaf(a, b, -p);   // r is exact; NaN beside an infinity, which stays
+  return fabsf(r) > 0.0f ? __uint_as_float(__float_as_uint(p) | 1u) : p;
+}
+
 // The codes of eight values over the scale s (none above it by more than the
 // rounding of top / R). Products by inv give the quotients within 3 ulp; if
 // one of them comes that near to a border between two codes, all eight are
@@ -377,7 +384,7 @@ __global__ void __launch_bounds__(kThreads) dequant_kv_kernel(const __grid_const
     Code<FMT>::decode4(c.x, t);
     Code<FMT>::decode4(c.y, t + 4);
 #pragma unroll
-    for (int e = 0; e < 8; ++e) t[e] *= sc;
+    for (int e = 0; e < 8; ++e) t[e] = product_to_odd(t[e], sc);
     *reinterpret_cast<uint4*>(p.out[which] + (int64_t(t0 + r) * p.n_kv_heads + h) * D + 8 * l) = pack8<T>(t);
   }
 }
