@@ -598,7 +598,7 @@ AWQ_API awq_status_t awq_kv_dequant(const awq_kv_cache_t* cache, const awq_kv_ba
  * the row's largest.
  * q, out [n_tokens][n_q_heads][head_dim]; n_q_heads a multiple of
  * n_kv_heads; window, sinks >= 0 (sinks is ignored without a window);
- * scale finite. out must not overlap q.
+ * |scale| below 2^118. out must not overlap q.
  * workspace: awq_kv_attention_workspace_bytes() bytes of device memory,
  * 16-byte aligned, contents irrelevant; the size depends on the shapes in
  * cache, batch and n_q_heads and on the device, not on the lengths. Nothing

@@ -138,6 +138,12 @@ def test_attention_checks(L):
     assert L.awq_kv_attention_workspace_bytes(ref(c), ref(b), 0, 4, ctypes.byref(n)) == OK and n.value == 0
 
 
+def test_logit_scales_that_overflow_in_log2_units(L):
+    """A finite scale whose multiple by log2(e) and e4m3's 2^8 is not: refused, where the kernels would give NaN."""
+    for scale in (3e38, -3e38, 2.0 ** 119, -2.0 ** 119):
+        assert attend(L, cache(), batch(), scale=scale) == SHAPE, scale
+
+
 def tensors(n=4, h=2, page=32, d=64):
     p = [torch.zeros(n, h, page, d, dtype=torch.uint8) for _ in range(2)]
     s = [torch.zeros(n, h, page // 16) for _ in range(2)]

@@ -993,7 +993,8 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   awq_status_t st = check_attention(cache, batch, n_tokens, n_q_heads);
   if (st != AWQ_OK) return st;
   if (!check_dtype(dtype)) return AWQ_ERR_UNSUPPORTED;
-  if (window < 0 || sinks < 0 || !(scale - scale == 0.0f)) return AWQ_ERR_SHAPE;
+  const float to_log2 = scale * kLog2e;   // the kernels multiply it by 2^8 (e4m3) and by block scales
+  if (window < 0 || sinks < 0 || !(to_log2 > -0x1p119f && to_log2 < 0x1p119f)) return AWQ_ERR_SHAPE;
   if (n_tokens == 0 || batch->n_seqs == 0) return AWQ_OK;
   if ((st = check_pointers(cache, batch)) != AWQ_OK) return st;
   if ((st = check_rows(q, q_stride, n_q_heads, cache->head_dim)) != AWQ_OK ||
@@ -1013,7 +1014,7 @@ extern "C" awq_status_t awq_kv_attention(const awq_kv_cache_t* cache, const awq_
   p.k_scales = cache->k_scales;
   p.v_scales = cache->v_scales;
   p.scale_stride = cache->scale_stride;
-  p.scale_log2 = scale * kLog2e;
+  p.scale_log2 = to_log2;
   // A window that no sequence can outgrow is none (and the kernels' differences of positions stay in 32 bits).
   p.window = int64_t(window) >= int64_t(batch->max_pages) * cache->page_size ? 0 : window;
   p.sinks = p.window ? sinks : 0;
