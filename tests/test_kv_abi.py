@@ -202,6 +202,18 @@ def test_binding_checks():
         awq.awq_kv_dequant(c, b, 3, torch.float32)
 
 
+def test_block_tables_of_one_page_may_have_any_column_stride():
+    """The stride of a dimension of one element means nothing."""
+    lens, ptr = torch.zeros(3, dtype=torch.int32), torch.zeros(4, dtype=torch.int32)
+    table = torch.arange(3, dtype=torch.int32)[None].t()
+    assert table.shape == (3, 1) and table.stride() == (1, 3)
+    b = awq.KvBatch(table, lens, ptr)
+    assert (b._args.table_stride, b._args.max_pages) == (1, 1)
+    with pytest.raises(ValueError):
+        awq.KvBatch(torch.zeros(3, 4, dtype=torch.int32).t()[:, :2], torch.zeros(4, dtype=torch.int32),
+                    torch.zeros(5, dtype=torch.int32))
+
+
 def test_oracle_encodes_the_nearest_code():
     """The oracle against the definition: no code is nearer, ties go to even."""
     rng = np.random.default_rng(1)

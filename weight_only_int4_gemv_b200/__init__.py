@@ -751,7 +751,7 @@ class KvBatch:
                 raise TypeError(f"{name} must be a torch.Tensor")
             if t.dtype != torch.int32:
                 raise TypeError(f"{name} must be torch.int32, got {t.dtype}")
-            if t.dim() != ndim or (t.numel() > 1 and t.stride(-1) != 1):
+            if t.dim() != ndim or (t.shape[-1] > 1 and t.stride(-1) != 1):
                 raise ValueError(f"{name} must be a {ndim}-d tensor with dense rows")
             if t.device != block_table.device:
                 raise ValueError(f"{name} is on {t.device}, block_table on {block_table.device}")
