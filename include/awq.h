@@ -472,7 +472,9 @@ AWQ_API awq_status_t awq_apply_clip(const uint16_t* W, const float* ratios, int6
  *   AWQ_KV_E4M3: s * e4m3(code); the codes 0x7f and 0xff (NaN) are not written
  *                for finite values, and attention over them is unspecified
  * A scale s is finite and 0 or positive. awq_kv_append writes none below 2^-60;
- * a cache filled otherwise may hold 0, with any code, for a block of zeros.
+ * a cache filled otherwise may hold 0, with any code, for a block of zeros
+ * (attention takes value scales below 2^-60 as 0). Beside such a block value
+ * scales above 2^40 cost its keys their part of the softmax.
  * NaN, an infinity or a negative number in place of a scale makes NaN of the
  * attention of every row and query head that sees the block, and of no other.
  * head_dim is 64 or 128; page_size a multiple of 16, up to 65536.

@@ -84,6 +84,24 @@ def test_scales_of_zero(rows, dtype, fmt, dim):
 
 
 @pytest.mark.parametrize("rows", KINDS)
+@pytest.mark.parametrize("dtype,fmt,dim", [("fp16", "int8", 128), ("bf16", "e4m3", 64)])
+@pytest.mark.parametrize("value", [2.0 ** -61, 2.0 ** -120, 1e-42])
+def test_value_scales_below_the_smallest(rows, dtype, fmt, dim, value):
+    """Blocks whose value scale lies below 2^-60, down to subnormal numbers, alone or beside others: their values count
+    as 0 (the oracle's are below 2^-52), their keys as they are."""
+    lens, new = [300, 84, 20], [rows, min(rows, 33), 1]
+    s = Setup(lens, 2, dim, 16, fmt, seed=48)
+    for b, i in [(0, 3), (0, 7), (0, 8), (1, 1), (2, 0), (2, 1)]:
+        s.ref.scales[1][int(s.table[b, i]), i % 2 if b < 2 else slice(None)] = value
+    put(s)
+    q = queries(s.rng, sum(new), 2, dim, dtype)
+    want, tol = s.expect(to64(q), lens, new)
+    assert (np.abs(want[-1]) < 2.0 ** -52).all()
+    check(attend(s, q, lens, new), want, tol)
+    assert awq.awq_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", KINDS)
 @pytest.mark.parametrize("which", ["k_scales", "v_scales"])
 @pytest.mark.parametrize("value", [float("nan"), float("inf"), float("-inf"), -1.0])
 @pytest.mark.parametrize("dtype,fmt", [("fp16", "int8"), ("bf16", "e4m3")])

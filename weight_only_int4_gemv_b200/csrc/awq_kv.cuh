@@ -15,7 +15,8 @@ constexpr uint32_t kErrWait = 8u;             // awq_device_error bit 3
 constexpr uint32_t kErrRange = 16u;           // awq_device_error bit 4
 // Smallest scale. A block of zeros needs a scale above 0, because the
 // attention adds log2 of the value scale to the logits; 2^-60 keeps its
-// reciprocal (and sums of 2^60 over any context) inside fp32. fp16 values
+// reciprocal (and sums of 2^60 over any context) inside fp32, and the weights
+// of such a block inside it beside blocks of scales up to 2^40. fp16 values
 // never reach it; bf16 values below 2^-61 become 0.
 constexpr float kScaleFloor = 8.673617379884035e-19f;
 

@@ -543,12 +543,13 @@ decode_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid_
         ks[u] = there ? me.ks[i] : 0.0f;
         const float to_log2 = p.scale_log2 * kShift<FMT>;   // (not into factor, which may be 2^126: keys of 0 have logits of 0)
         float vs = there ? me.vs[i] : 1.0f;
-        // values of scale 0 are 0 whatever their codes: no weight in O; in l they have their keys', by the smallest scale
-        held[u] = vs == 0.0f ? 0u : ~0u;
-        vs = vs == 0.0f ? kScaleFloor : vs;
         // a scale that is no finite number of at least 0 makes NaN of the logits, which the rows that do not see the
         // block mask (an infinite one times a negative S would be a weight of 0 instead)
         const bool fine = ks[u] >= 0.0f && vs >= 0.0f && ks[u] + vs < INFINITY;
+        // values of scale 0 (or below the smallest, which would leave fp32's range here) are 0 whatever their codes: no
+        // weight in O; in l they have their keys', by the smallest scale
+        held[u] = vs < kScaleFloor ? 0u : ~0u;
+        vs = fmaxf(vs, kScaleFloor);
         ks[u] *= to_log2;
         lv[u] = fine ? __log2f(vs) : __int_as_float(0x7fffffff);
         iv[u] = fine ? __fdividef(1.0f / kShift<FMT>, vs) : 0.0f;   // (O holds codes / kShift)

@@ -580,7 +580,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
       const PreMeta& me = sh.meta[mi];
       const int flags = me.flags;
       if (flags & kStop) break;
-      const unsigned zeros = __ballot_sync(0xffffffffu, lane < 8 && me.vs[lane & 7] == 0.0f);
+      const unsigned zeros = __ballot_sync(0xffffffffu, lane < 8 && me.vs[lane & 7] < kScaleFloor);
       if (tid < 8) {                             // (published with the keys)
         PreMeta& out = sh.meta[mi];
         // A scale that is no finite number of at least 0 must not reach the rows that do not see its block (there t is -inf by S, whatever
@@ -589,8 +589,9 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
         const bool fine = ks >= 0.0f && vs >= 0.0f && ks + vs < INFINITY;
         const float a = fine ? fmaxf(fabsf(p.scale_log2) * kShift<FMT> * ks, kLeastA) : kLeastA;
         out.a[tid] = p.scale_log2 < 0.0f ? -a : a;
-        // (a scale of 0 counts as the smallest one here, which gives its keys their mass; its codes are made 0 below)
-        const float v = vs == 0.0f ? kScaleFloor : vs;
+        // (a scale of 0, or below the smallest, counts as that here, which gives its keys their mass; its codes are made
+        // 0 below)
+        const float v = fmaxf(vs, kScaleFloor);
         out.lv[tid] = fine ? __log2f(v) : kSpoilt;
         out.iv[tid] = fine ? __fdividef(1.0f / kShift<FMT>, v) : 1.0f;   // (O holds codes / kShift)
       }
@@ -615,7 +616,7 @@ prefill_attention_kernel(const __grid_constant__ CUtensorMap map_k, const __grid
           *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c0) = a;
           *reinterpret_cast<uint4*>(half + i * kRowStep * 128 + c1) = b;
         }
-        if (kv && zeros) {                        // values of scale 0 are 0, whatever their codes
+        if (kv && zeros) {                        // values of scale 0, whatever their codes
 #pragma unroll 1
           for (int i = 0; i < kTile / kRowStep; ++i)
             if ((zeros >> ((r0 + i * kRowStep) / kBlock)) & 1u)
