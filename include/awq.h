@@ -531,7 +531,7 @@ typedef struct awq_kv_batch {
   const int32_t* q_indptr;      /* [n_seqs + 1] */
   int64_t table_stride;
   int32_t n_seqs;
-  int32_t max_pages;
+  int32_t max_pages;            /* short batches run faster with no more than the longest needs */
   int32_t max_q_len;            /* bound on every n_b; 0: n_tokens is the bound */
 } awq_kv_batch_t;
 

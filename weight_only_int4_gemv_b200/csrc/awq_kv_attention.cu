@@ -38,11 +38,11 @@
 // tiles of each stage, each with its own m, l and O, joined at the item's end.
 //
 // Measured on one B200 (a Python call, launches included): 32 sequences of up
-// to 8192 tokens, 32 / 8 heads of 128, int8 (276 MB) 61 us, 4.5 TB/s; two of
-// up to 131001, 64 / 8 heads, e4m3 (381 MB) 85 us, 4.5 TB/s; 48 sequences of
-// 5 rows, 16 heads of 64 (197 MB) 51 us, 3.8 TB/s; one of 777 tokens 13 us, 10
-// of them on the GPU. The same copies with no arithmetic: 60, 71, 57 us before
-// the items' cost was counted (then 71, 91, 77 with it).
+// to 8192 tokens, 32 / 8 heads of 128, int8 (276 MB) 59 us, 4.7 TB/s; two of
+// up to 131001, 64 / 8 heads, e4m3 (381 MB) 87 us, 4.4 TB/s; 48 sequences of
+// 5 rows, 16 heads of 64 (197 MB) 53.5 us, 3.7 TB/s; one of 777 tokens 13.5 us,
+// 9 of them on the GPU. The same copies with no arithmetic: 60, 71, 57 us
+// before the items' cost was counted (then 71, 91, 77 with it).
 
 #include <cuda.h>
 #include <cudaTypedefs.h>
@@ -64,9 +64,9 @@ constexpr int kThreads = (W + 1) * 32;
 constexpr int U = 2;                       // tiles of a warp in a stage
 constexpr int WT = W * U;                  // tiles of a stage
 constexpr int kStages = 2;
-// What an item costs a CTA beyond its tiles (q rows, the warps' joining, output), in tiles: the cut counts every item
-// as that much longer. (0, 4, 8, 14: 128 sequences of up to 128 tokens 33, 20, 18, 16 us; 32 of up to 2000 25, 23, 27,
-// 20; 48 sequences of 5 rows over 4000 73, 57, 52, 52.)
+// What an item costs a CTA beyond its tiles (q rows, the warps' joining, output), in tiles: the cut counts every item as
+// that much longer. (On the GPU, 0, 8, 12, 14: 128 sequences of up to 128 tokens 30, 17, 16, 21 us; 32 of up to 2000 32,
+// 18, 20, 24, e4m3 and groups of 8 39, 22, 22, 28; 48 sequences of 5 rows over 4000, heads of 64, 64, 48, 54, 51.)
 constexpr int kItemCost = 12;
 constexpr int kItems = 8;                  // more than the stages in the ring and the one ahead of it
 constexpr float kLog2e = 1.4426950408889634f;
@@ -893,11 +893,15 @@ size_t workspace_of(const Variant& v, int grid, int d) {
 
 // The kernel, by the rows (tokens x group) of the longest sequence and the (rows of the call) x (tiles of 16 keys that
 // fit a sequence): tiles of 8 rows while they fit one; beyond, tiles of 16, which read the cache once each but start
-// fast and share the work finely, until the pairs of 128 on the tensor cores win. Measured (32 / 8 heads of 128, int8;
-// tiles of 16 and pairs of 128, us):
-//   16 sequences of 2000 tokens, 48 and 96 rows each:       35 and 51, 54 and 51
-//   1 sequence, 240 rows, 60, 2000, 8000 tokens:            7 and 16, 24 and 30, 58 and 43
-//   1 sequence, 480 rows, 120, 2000 tokens:                 9 and 16, 38 and 30
+// fast and share the work finely, until the pairs of 128 on the tensor cores win. Measured on the GPU (tiles of 16 and
+// pairs of 128, us; the product of rows and tiles in brackets):
+//   32 / 8 heads of 128, int8: 60 tokens of a prompt of 60, 2000, 8000 [1200, 30960, 120240] 7 and 15, 24 and 28, 59
+//   and 41; prompts of 128, 256, 512 [4608, 17408, 67584] 8.5 and 15, 22 and 22, 47 and 27. e4m3: within 15 % of these.
+//   16 heads of 64, group 1, int8: prompts of 128, 256, 512 [1152, 4352, 16896] 6 and 11, 8 and 15, 23 and 19
+//   16 key heads of 64, group 4, e4m3: prompts of 128, 256, 512 [4608, 17408, 67584] 14 and 14, 25 and 20, 65 and 27
+// The border lies higher with few key heads and lower with many short sequences, which the rule does not know:
+//   1 key head of 128, group 8: 60 tokens of 8000 [240480] 25 and 71, prompts of 512 [135168] 14 and 22
+//   8 prompts of 100, 32 / 8 heads [28800] 35 and 17; 16 / 16 heads of 64 [7200] 19 and 13
 int kind_of(int64_t rows, int64_t all, int64_t tiles) { return rows <= 8 ? 0 : rows <= 64 || all * tiles <= 32768 ? 1 : 2; }
 
 awq_status_t check_attention(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens,
@@ -918,10 +922,11 @@ struct Plan {
 };
 
 // Up to how many tiles an item is taken whole by one CTA, without parts and the kernel that joins them, when there is
-// a CTA for every item. Measured (32 / 8 heads of 128, int8; whole and split, us):
-//   1 sequence of 128, 500, 1000 tokens:   5.6 and 6.9, 9.5 and 7.9, 15 and 10
-//   8 sequences of up to 128, 500, 1000:   6.8 and 10, 10 and 12, 16 and 12
-//   32 sequences of up to 128, 500, 1000:  7.7 and 13, 12 and 17, 19 and 20
+// a CTA for every item. The tiles are those that the table has room for: with a table of 131072 tokens nothing is taken
+// whole. Measured on the GPU (32 / 8 heads of 128, int8; whole and split, us):
+//   1 sequence of 128, 500, 1000 tokens:   5.6 and 7.6, 9.5 and 7.9, 15 and 10
+//   8 sequences of up to 128, 500, 1000:   6.6 and 8.8, 10 and 12, 16 and 12
+//   32 sequences of up to 128, 500, 1000:  7.7 and 9.4, 12.8 and 12.1, 19 and 20
 int whole_tiles(int64_t items, int grid) { return items > grid ? 0 : items * 2 >= grid ? 64 : items * 8 >= grid ? 40 : 24; }
 
 awq_status_t plan_of(const awq_kv_cache_t* cache, const awq_kv_batch_t* batch, int64_t n_tokens, int32_t dtype,

@@ -32,14 +32,17 @@
 // as for few rows; split items meet in join_rows_kernel.
 //
 // Measured on one B200: chunks of up to 509 rows x 8 heads over up to 6001
-// tokens, 8 key / value heads of 128, e4m3: 224 us, 681 TFLOP/s (40 % of a
-// dense bf16 product's measured rate); a prompt of 2048, 32 / 8 heads, int8: 69
-// us, 494 TFLOP/s; 4096 with a window of 1024: 125 us, 483. Two thirds of the
-// tensor pipe's cycles are idle: S -> softmax -> P -> next S is a chain of
-// latencies (softmax 2800 to 3900 cycles, both products 2000) with two row
-// tiles in flight, and tensor memory has no room for a third. The exponential
-// unit is not the bound: every fourth (third, second) pair of exponentials as
-// a polynomial on the FMA pipe took 71 (71, 74) us for the prompt.
+// tokens, 8 key / value heads of 128, e4m3: 225 us, 679 TFLOP/s (40 % of a
+// dense bf16 product's measured rate); a prompt of 2048, 32 / 8 heads, int8: 70
+// us, 490 TFLOP/s; 4096 with a window of 1024: 126 us, 478. Two thirds of the
+// tensor pipe's cycles are idle: a tile's softmax takes 2800 to 3900 cycles,
+// its products 2000 and its exponentials alone about 1000. What stands between
+// is exposed latency: S is read in steps of 32 columns, each waited for, once
+// for the maximum and again for the weights; the halves of all rows of a row
+// tile meet in between; the second product starts when all of P is there. The
+// exponential unit is not the bound: every fourth (third, second) pair of
+// exponentials as a polynomial on the FMA pipe took 71 (71, 74) us for the
+// prompt.
 
 constexpr int kTile = 128;                     // keys of a tile, and rows of a row tile
 constexpr int kPairRows = 2 * kTile;
