@@ -7,7 +7,7 @@ import pytest
 import torch
 
 import weight_only_int4_gemv_b200 as awq
-from kv_util import DT, Setup, check, to64
+from kv_util import DT, Setup, check, i32, to64
 from test_gpu_kv_attention import queries
 
 pytestmark = pytest.mark.gpu
@@ -238,3 +238,113 @@ def test_dequant_rounds_once(fmt, dtype):
         e = np.maximum(np.floor(np.log2(np.abs(np.where(exact == 0, 1.0, exact)))), lowest) - (mantissa - 1)
         want = np.rint(exact / 2.0 ** e) * 2.0 ** e       # a power of two divides exactly; ties to even
         assert np.array_equal(to64(y), want), f"{(to64(y) != want).sum()} values"
+
+
+@pytest.mark.parametrize("rows", KINDS)
+@pytest.mark.parametrize("pad", [8, 16])
+@pytest.mark.parametrize("dtype,fmt,dim", [("fp16", "int8", 64), ("bf16", "e4m3", 128)])
+def test_strided_outputs_of_a_layer_among_others(rows, pad, dtype, fmt, dim):
+    """Rows of out that are columns of wider ones (at 16 and at 32 bytes' alignment), a block table that is a slice, a
+    cache that is one layer of an array: the bits of the dense call, and nothing beside the columns written."""
+    lens, new = [700, 130, 40], [rows, min(rows, 130), 0]
+    s = Setup(lens, 2, dim, 32, fmt, seed=49, layers=3)
+    q = queries(s.rng, sum(new), 6, dim, dtype)
+    many = rows * 3 > 64
+    extra = 40000 // s.page if many else 3
+    table = torch.cat((torch.from_numpy(s.table), torch.full((3, extra + 5), -1, dtype=torch.int32)), 1).cuda()
+    batch = awq.KvBatch(table[:, :s.table.shape[1] + extra], i32(lens), i32(np.concatenate([[0], np.cumsum(new)])), rows)
+    assert is_many(s.cache, batch, sum(new), 6) == many
+    want, tol = s.expect(to64(q), lens, new)
+    dense = awq.awq_kv_attention(q, s.cache, batch)
+    check(dense, want, tol)
+    buffer = torch.full((sum(new), 6 * dim + 2 * pad), 3.0, dtype=q.dtype, device="cuda")
+    out = buffer[:, pad:-pad].unflatten(1, (6, dim))
+    assert awq.awq_kv_attention(q, s.cache, batch, out=out) is out
+    assert torch.equal(out, dense)
+    assert (buffer[:, :pad] == 3.0).all() and (buffer[:, -pad:] == 3.0).all()
+
+
+@pytest.mark.parametrize("rows", KINDS)
+def test_batches_without_rows_of_any_sequence(rows):
+    """All sequences bring 0 rows: nothing is written, nothing recorded."""
+    s = Setup([100, 64], 2, 64, 16, "int8", seed=50)
+    q = queries(s.rng, rows, 2, 64, "fp16")
+    kept = [t.clone() for t in (s.cache.k_pages, s.cache.v_pages, s.cache.k_scales, s.cache.v_scales)]
+    for lens in ([100, 64], [0, 0]):
+        for n in (1, 2):
+            batch = awq.KvBatch(torch.from_numpy(s.table[:n]).cuda(), i32(lens[:n]), i32([0] * (n + 1)), rows)
+            for b in (batch, s.batch(lens, [0, 0], rows, wide=True)):
+                out = torch.full_like(q, 5.0)
+                awq.awq_kv_attention(q, s.cache, b, out=out)
+                turned = awq.awq_kv_append(q, q, s.cache, b, q=q, q_out=torch.full_like(q, 5.0))
+                back = awq.awq_kv_dequant(s.cache, b, rows, q.dtype, torch.full_like(q, 5.0), torch.full_like(q, 5.0))
+                for t in (out, turned, *back):
+                    assert (t == 5.0).all()
+    assert awq.awq_device_error() == 0
+    for a, b in zip(kept, (s.cache.k_pages, s.cache.v_pages, s.cache.k_scales, s.cache.v_scales)):
+        assert torch.equal(a, b)
+
+
+def test_more_rows_than_the_bound_said():
+    """max_q_len chooses the kernel and nothing else."""
+    lens, new = [333, 90], [140, 3]
+    s = Setup(lens, 2, 128, 16, "int8", seed=51)
+    q = queries(s.rng, sum(new), 8, 128, "fp16")
+    want, tol = s.expect(to64(q), lens, new)
+    for bound in (1, 4, 16, 140, None):
+        for wide in (False, True):
+            check(awq.awq_kv_attention(q, s.cache, s.batch(lens, new, bound, wide=wide)), want, tol, f"{bound} {wide}")
+    assert awq.awq_device_error() == 0
+
+
+@pytest.mark.parametrize("rows", KINDS)
+@pytest.mark.parametrize("window,sinks", [(5, 2 ** 31 - 1), (2 ** 31 - 1, 2 ** 31 - 1), (399, 0), (400, 1), (1, 399)])
+def test_windows_and_sinks_of_any_size(rows, window, sinks):
+    lens, new = [400, 80], [rows, min(rows, 80)]
+    s = Setup(lens, 2, 64, 16, "e4m3", seed=52)
+    q = queries(s.rng, sum(new), 2, 64, "bf16")
+    want, tol = s.expect(to64(q), lens, new, window=window, sinks=sinks)
+    check(attend(s, q, lens, new, window=window, sinks=sinks), want, tol)
+
+
+@pytest.mark.parametrize("fmt", ["int8", "e4m3"])
+def test_append_takes_and_gives_strided_rows(fmt):
+    """k, v, q and q_out as columns of wider rows, of which nothing else is written; a captured append and read-back,
+    replayed on a stream of its own."""
+    lens, new = [50, 33], [20, 33]
+    made = []
+    for strided in (False, True):
+        s = Setup(lens, 2, 128, 16, fmt, seed=53, layers=2)
+        x = torch.from_numpy(s.rng.standard_normal((53, 8, 128))).cuda().half()
+        q, k, v = (t.contiguous() for t in x.split((4, 2, 2), 1))
+        out = torch.zeros_like(q)
+        if strided:
+            rows = torch.full((53, 8 * 128 + 24), 9.0, dtype=torch.float16, device="cuda")
+            q, k, v = (rows[:, a:a + t[0].numel()].unflatten(1, t.shape[1:]).copy_(t)
+                       for a, t in ((8, q), (8 + 512, k), (16 + 768, v)))
+            wide = torch.full((53, 4 * 128 + 16), 9.0, dtype=torch.float16, device="cuda")
+            out = wide[:, 8:-8].unflatten(1, (4, 128))
+        batch = s.batch(lens, new)
+        back = [torch.zeros(53, 2, 128, dtype=torch.float16, device="cuda") for _ in range(2)]
+
+        def step():
+            awq.awq_kv_append(k, v, s.cache, batch, q=q, q_out=out)
+            awq.awq_kv_dequant(s.cache, batch, 53, torch.float16, *back)
+
+        if strided:
+            side = torch.cuda.Stream()
+            side.wait_stream(torch.cuda.current_stream())
+            with torch.cuda.stream(side):
+                graph = torch.cuda.CUDAGraph()
+                with torch.cuda.graph(graph, stream=side):
+                    step()
+                graph.replay()
+                graph.replay()
+            torch.cuda.current_stream().wait_stream(side)
+            assert (wide[:, :8] == 9.0).all() and (wide[:, -8:] == 9.0).all()
+        else:
+            step()
+        made.append([t.clone() for t in (s.cache.k_pages, s.cache.v_pages, s.cache.k_scales, s.cache.v_scales, out, *back)])
+    for a, b in zip(*made):
+        assert torch.equal(a, b)
+    assert awq.awq_device_error() == 0
